@@ -301,7 +301,7 @@ def _plain_verify(s):
     left = torch.where(rejected[:, None], left, p).clamp(min=0)
     left = torch.where(left.sum(1, keepdim=True) > 0, left, p)
     run_sum = torch.cumsum(left, 1)
-    beyond = run_sum > s["u"][at, good].double()[:, None] * run_sum[:, -1:]
+    beyond = run_sum > s["u"][:, d].double()[:, None] * run_sum[:, -1:]
     pick = (beyond & (left > 0)).long().argmax(1)
     col = torch.arange(d + 1, device=tok.device)[None, :]
     drafted = torch.cat([tok, tok[:, :1]], 1)
