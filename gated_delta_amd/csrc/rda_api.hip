@@ -30,6 +30,79 @@ bool overlap(Range x, Range y) {
     return x.lo < y.hi && y.lo < x.hi;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rows of `width` 16-bit values, `stride` values apart: 16-byte rows, and
+// 64 of them within 32-bit byte offsets.
+bool stride_ok(int64_t stride, int64_t width) {
+    return stride >= width && stride % 8 == 0 && stride <= (int64_t(1) << 24);
+}
+
+size_t rows_bytes(int64_t rows, int64_t stride, int64_t width) {
+    return rows > 0 ? (size_t(rows - 1) * size_t(stride) + size_t(width)) * 2 : 0;
+}
+
+rda_status check_pages(int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                       int32_t table_width) {
+    if (num_pages < 0 || table_width < 0 || page_tokens < 1) return RDA_ERR_SHAPE;
+    if (page_tokens < RDA_MLA_MIN_PAGE || page_tokens > RDA_MLA_MAX_PAGE ||
+        (page_tokens & (page_tokens - 1)))
+        return RDA_ERR_UNSUPPORTED;
+    if (page_stride < int64_t(page_tokens) * RDA_MLA_ROW || page_stride % 8 ||
+        page_stride > (int64_t(1) << 40))
+        return RDA_ERR_SHAPE;
+    return RDA_OK;
+}
+
+rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, int32_t prefix_len) {
+    if (batch < 0 || tokens < 0 || tokens > RDA_DECODE_MAX_TOKENS || heads < 1 || prefix_len < 0)
+        return RDA_ERR_SHAPE;
+    // 32-bit indexes of query rows and of tiles
+    if (int64_t(tokens) * heads > (1 << 24) ||
+        int64_t(batch) * tokens * heads > (1 << 26) || prefix_len > (1 << 30))
+        return RDA_ERR_SHAPE;
+    return RDA_OK;
+}
+
+// The plan of rda_mla_decode (sizes in A) and its workspace: with ws, the
+// pointers too.  Returns the bytes.
+//
+// Query rows go in blocks of 64 (two row groups) where a sequence has more
+// than 32, in blocks of 32 otherwise.  Every workgroup takes an equal share
+// of the tiles, but at least min_tiles: a share that small costs more in
+// partial sums (64 KiB per 32 rows) than in tiles (36 KiB each).
+size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
+    const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
+    A.row_groups = unit_rows > 32 ? 2 : 1;
+    A.row_blocks = int32_t((unit_rows + 32 * A.row_groups - 1) / (32 * A.row_groups));
+    A.min_tiles = 4;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char* p = ws ? ws + at : nullptr;
+        at += align256(bytes);
+        return p;
+    };
+    const size_t units = size_t(A.batch) * A.row_blocks;
+    A.meta = reinterpret_cast<int32_t*>(take(units * 2 * sizeof(int32_t)));
+    const size_t slots = (units + kMlaWorkgroups) * 32 * A.row_groups;
+    A.part = reinterpret_cast<float*>(take(slots * RDA_MLA_LATENT * sizeof(float)));
+    A.part_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
+    A.prefix_groups = 1;
+    A.prefix_units = 0;
+    A.prefix_per = 1;
+    if (A.prefix_len > 0 && rows > 0) {
+        A.prefix_groups = rows > 32 ? 2 : 1;
+        A.prefix_units = int32_t((rows + 32 * A.prefix_groups - 1) / (32 * A.prefix_groups));
+        const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
+        const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
+        A.prefix_per = share > 8 ? share : 8;
+        const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_groups;
+        A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
+        A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));
+    }
+    return at;
+}
+
 constexpr int kWalkSlices = kD / 16;  // value-channel slices per (sequence, head)
 
 // The segmented state pass for one long sequence with few heads.  The walk
@@ -975,6 +1048,222 @@ rda_status rda_decode_tokens_diag(const void* q, const void* k, const void* v,
                                   const int32_t* accept, float* o, hipStream_t stream) {
     return decode_tokens_any(q, k, v, qkv_dtype, alpha, b, batch, tokens, num_heads, dk, dv,
                              S_in, S_out, accept, o, true, stream);
+}
+
+rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int64_t kv_stride,
+                           const void* k_pe, int64_t pe_stride, const int32_t* cu_q,
+                           const int32_t* cu_k, int32_t num_seqs, int32_t total_q,
+                           int32_t total_k, int32_t num_heads, float scale, int32_t causal,
+                           void* o, float* lse, hipStream_t stream) {
+    if (num_seqs < 1 || total_q < 0 || total_k < 0 || num_heads < 1) return RDA_ERR_SHAPE;
+    if ((!cu_q && (cu_k || num_seqs != 1)) || (cu_q && !cu_k && total_k != total_q))
+        return RDA_ERR_SHAPE;
+    const int64_t H = num_heads;
+    if (!stride_ok(q_stride, H * RDA_MLA_QK) || !stride_ok(kv_stride, H * RDA_MLA_KV) ||
+        !stride_ok(pe_stride, RDA_MLA_PE))
+        return RDA_ERR_SHAPE;
+    const int64_t slots = mla_prefill_slots(total_q, num_seqs);
+    if (slots * H > INT32_MAX) return RDA_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return RDA_ERR_VALUE;
+    if (total_q == 0) return RDA_OK;
+    if (!q || !o || (total_k > 0 && (!kv || !k_pe))) return RDA_ERR_NULL;
+    for (const void* p : {q, kv, k_pe, static_cast<const void*>(o)})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(cu_q), static_cast<const void*>(cu_k),
+                          static_cast<const void*>(lse)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    const size_t ni = size_t(num_seqs + 1) * 4;
+    const Range in[] = {rng(q, rows_bytes(total_q, q_stride, H * RDA_MLA_QK)),
+                        rng(kv, rows_bytes(total_k, kv_stride, H * RDA_MLA_KV)),
+                        rng(k_pe, rows_bytes(total_k, pe_stride, RDA_MLA_PE)),
+                        rng(cu_q, ni), rng(cu_k, ni)};
+    const Range ro = rng(o, size_t(total_q) * H * RDA_MLA_V * 2);
+    const Range rl = rng(lse, size_t(total_q) * H * 4);
+    if (overlap(ro, rl)) return RDA_ERR_ALIAS;
+    for (const Range& r : in)
+        if (overlap(ro, r) || overlap(rl, r)) return RDA_ERR_ALIAS;
+    MlaPrefillArgs A{};
+    A.q = static_cast<const uint16_t*>(q);
+    A.kv = static_cast<const uint16_t*>(kv);
+    A.pe = static_cast<const uint16_t*>(k_pe);
+    A.q_stride = q_stride;
+    A.kv_stride = kv_stride;
+    A.pe_stride = pe_stride;
+    A.cu_q = cu_q;
+    A.cu_k = cu_q && !cu_k ? cu_q : cu_k;
+    A.num_seqs = num_seqs;
+    A.total_q = total_q;
+    A.total_k = total_k;
+    A.heads = num_heads;
+    A.slots = int32_t(slots);
+    A.scale = scale;
+    A.causal = causal;
+    A.o = static_cast<uint16_t*>(o);
+    A.lse = lse;
+    return launch_mla_prefill(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+}
+
+size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
+                                      int32_t prefix_len) {
+    MlaDecodeArgs A{};
+    if (check_mla_decode_sizes(batch, tokens, num_heads, prefix_len) != RDA_OK) return 0;
+    A.batch = batch;
+    A.tokens = tokens;
+    A.heads = num_heads;
+    A.prefix_len = prefix_len;
+    return mla_decode_plan(A, nullptr);
+}
+
+rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
+                          int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                          const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
+                          int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (rda_status st = check_mla_decode_sizes(batch, tokens, num_heads, prefix_len); st != RDA_OK)
+        return st;
+    if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
+        return st;
+    if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return RDA_ERR_VALUE;
+    if (batch == 0 || tokens == 0) return RDA_OK;
+    if (!q || !o || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache) ||
+        (prefix_len > 0 && !prefix_table))
+        return RDA_ERR_NULL;
+    for (const void* p : {q, cache, static_cast<const void*>(o)})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(kv_lens),
+                          static_cast<const void*>(prefix_table), static_cast<const void*>(lse)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    MlaDecodeArgs A{};
+    A.batch = batch;
+    A.tokens = tokens;
+    A.heads = num_heads;
+    A.prefix_len = prefix_len;
+    const size_t need = mla_decode_plan(A, nullptr);
+    if (!workspace || workspace_bytes < need) return RDA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return RDA_ERR_ALIGN;
+    mla_decode_plan(A, static_cast<unsigned char*>(workspace));
+    const size_t rows = size_t(batch) * tokens * num_heads;
+    const Range in[] = {rng(q, rows * RDA_MLA_ROW * 2),
+                        rng(cache, rows_bytes(num_pages, page_stride, int64_t(page_tokens) * RDA_MLA_ROW)),
+                        rng(block_table, size_t(batch) * table_width * 4), rng(kv_lens, size_t(batch) * 4),
+                        rng(prefix_table, (size_t(prefix_len) + page_tokens - 1) / page_tokens * 4)};
+    const Range out[] = {rng(o, rows * RDA_MLA_LATENT * 2), rng(lse, rows * 4), rng(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(out[i], r)) return RDA_ERR_ALIAS;
+        if (overlap(out[i], out[(i + 1) % 3])) return RDA_ERR_ALIAS;
+    }
+    A.q = static_cast<const uint16_t*>(q);
+    A.cache = static_cast<const uint16_t*>(cache);
+    A.page_stride = page_stride;
+    A.num_pages = num_pages;
+    A.page_shift = __builtin_ctz(unsigned(page_tokens));
+    A.table = block_table;
+    A.table_width = table_width;
+    A.kv_lens = kv_lens;
+    A.prefix_table = prefix_table;
+    A.scale = scale;
+    A.o = static_cast<uint16_t*>(o);
+    A.lse = lse;
+    return launch_mla_decode(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+}
+
+rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight, float eps,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                          const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
+                          void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                          hipStream_t stream) {
+    if (num_seqs < 1 || total_tokens < 0 || (!cu_seqlens && total_tokens % num_seqs))
+        return RDA_ERR_SHAPE;
+    if (!stride_ok(kv_stride, RDA_MLA_ROW)) return RDA_ERR_SHAPE;
+    if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
+        return st;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return RDA_ERR_VALUE;
+    if (total_tokens == 0) return RDA_OK;
+    if (!kv || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache))
+        return RDA_ERR_NULL;
+    for (const void* p : {kv, static_cast<const void*>(weight), static_cast<const void*>(cache)})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(cu_seqlens), static_cast<const void*>(kv_lens),
+                          static_cast<const void*>(block_table)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    const Range rc = rng(cache, rows_bytes(num_pages, page_stride, int64_t(page_tokens) * RDA_MLA_ROW));
+    for (const Range& r : {rng(kv, rows_bytes(total_tokens, kv_stride, RDA_MLA_ROW)),
+                           rng(weight, RDA_MLA_LATENT * 4), rng(cu_seqlens, size_t(num_seqs + 1) * 4),
+                           rng(kv_lens, size_t(num_seqs) * 4),
+                           rng(block_table, size_t(num_seqs) * table_width * 4)})
+        if (overlap(rc, r)) return RDA_ERR_ALIAS;
+    if (num_pages == 0 || table_width == 0) return RDA_OK;
+    MlaAppendArgs A{};
+    A.kv = static_cast<const uint16_t*>(kv);
+    A.kv_stride = kv_stride;
+    A.weight = weight;
+    A.eps = eps;
+    A.cu = cu_seqlens;
+    A.kv_lens = kv_lens;
+    A.table = block_table;
+    A.num_seqs = num_seqs;
+    A.total = total_tokens;
+    A.table_width = table_width;
+    A.cache = static_cast<uint16_t*>(cache);
+    A.page_stride = page_stride;
+    A.num_pages = num_pages;
+    A.page_shift = __builtin_ctz(unsigned(page_tokens));
+    return launch_mla_append(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+}
+
+size_t rda_verify_drafts_workspace_bytes(int32_t batch, int32_t vocab) {
+    if (batch < 0 || vocab < 1) return 0;
+    return align256(size_t(batch) * verify_chunks(vocab) * 2 * sizeof(double));
+}
+
+rda_status rda_verify_drafts(const float* target, int64_t target_stride, const float* draft,
+                             int64_t draft_stride, const int32_t* draft_tokens,
+                             const float* uniforms, const int32_t* num_drafts, int32_t batch,
+                             int32_t drafts, int32_t vocab, int32_t* accept, int32_t* out_tokens,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (batch < 0 || batch > 65535 || drafts < 0 || drafts >= RDA_DECODE_MAX_TOKENS || vocab < 1)
+        return RDA_ERR_SHAPE;
+    if (target_stride < vocab || (draft && draft_stride < vocab)) return RDA_ERR_SHAPE;
+    if (batch == 0) return RDA_OK;
+    if (!target || !uniforms || !accept || !out_tokens || (drafts > 0 && !draft_tokens))
+        return RDA_ERR_NULL;
+    const size_t need = rda_verify_drafts_workspace_bytes(batch, vocab);
+    if (!workspace || workspace_bytes < need) return RDA_ERR_WORKSPACE;
+    for (const void* p : {static_cast<const void*>(target), static_cast<const void*>(draft),
+                          static_cast<const void*>(workspace)})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(draft_tokens), static_cast<const void*>(uniforms),
+                          static_cast<const void*>(num_drafts), static_cast<const void*>(accept),
+                          static_cast<const void*>(out_tokens)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    const size_t B = size_t(batch), T = size_t(drafts) + 1;
+    const Range in[] = {rng(target, rows_bytes(int64_t(B * T), target_stride, vocab) * 2),
+                        rng(draft, draft ? rows_bytes(int64_t(B * drafts), draft_stride, vocab) * 2 : 0),
+                        rng(draft_tokens, B * drafts * 4), rng(uniforms, B * T * 4),
+                        rng(num_drafts, B * 4)};
+    const Range out[] = {rng(accept, B * 4), rng(out_tokens, B * T * 4), rng(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(out[i], r)) return RDA_ERR_ALIAS;
+        if (overlap(out[i], out[(i + 1) % 3])) return RDA_ERR_ALIAS;
+    }
+    VerifyArgs A{};
+    A.target = target;
+    A.draft = drafts > 0 ? draft : nullptr;
+    A.target_stride = target_stride;
+    A.draft_stride = draft_stride;
+    A.tokens = draft_tokens;
+    A.uniforms = uniforms;
+    A.num_drafts = num_drafts;
+    A.batch = batch;
+    A.drafts = drafts;
+    A.vocab = vocab;
+    A.accept = accept;
+    A.out = out_tokens;
+    A.sums = static_cast<double*>(workspace);
+    return launch_verify(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
 }
 
 rda_status rda_chunk_table(const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,

@@ -311,4 +311,83 @@ hipError_t launch_walk_bf16(const uint16_t* q, const uint16_t* k, const uint16_t
 hipError_t launch_segment_combine(const float* S0, const float* E, const float* M, float* S_in,
                                   float* S_final, int32_t P, int32_t heads, hipStream_t stream);
 
+// Expanded latent attention over packed prompts.
+struct MlaPrefillArgs {
+    const uint16_t* q;         // [Tq] rows of q_stride values, head h at 192 h
+    const uint16_t* kv;        // [Tk] rows of kv_stride values, head h at 256 h (keys, values)
+    const uint16_t* pe;        // [Tk] rows of pe_stride values: the shared key channels
+    int64_t q_stride, kv_stride, pe_stride;
+    const int32_t* cu_q;       // [N+1] or nullptr (one sequence)
+    const int32_t* cu_k;
+    int32_t num_seqs, total_q, total_k, heads;
+    int32_t slots;             // mla_prefill_slots(total_q, num_seqs)
+    float scale;
+    int32_t causal;
+    uint16_t* o;               // [Tq, H, 128]
+    float* lse;                // [Tq, H] or nullptr
+};
+// Query-tile slots of a packed batch (an upper bound on its tiles).
+int64_t mla_prefill_slots(int32_t total_q, int32_t num_seqs);
+hipError_t launch_mla_prefill(const MlaPrefillArgs& A, hipStream_t stream);
+
+// Absorbed latent attention over a paged cache of latent rows.
+constexpr int kMlaWorkgroups = 256;   // one per CU: its tiles fill a CU's LDS
+struct MlaDecodeArgs {
+    const uint16_t* q;           // [B, T, H, 576]
+    const uint16_t* cache;       // pages of page_stride values, rows of 576
+    int64_t page_stride;
+    int32_t num_pages, page_shift;
+    const int32_t* table;        // [B, table_width] page ids
+    int32_t table_width;
+    const int32_t* kv_lens;      // [B]
+    const int32_t* prefix_table; // page ids of the shared rows
+    int32_t prefix_len;
+    int32_t batch, tokens, heads;
+    float scale;
+    uint16_t* o;                 // [B, T, H, 512]
+    float* lse;                  // [B, T, H] or nullptr
+    // plan (mla_decode_plan): a sequence's query rows in row_blocks blocks of
+    // 32 row_groups, all query rows in prefix_units blocks of 32 prefix_groups
+    int32_t row_groups, row_blocks, min_tiles;
+    int32_t prefix_groups, prefix_units;
+    int64_t prefix_per;          // prefix tiles per workgroup
+    // workspace
+    int32_t* meta;               // per unit: first and last workgroup, or -1
+    float *part, *part_ml, *pre_part, *pre_ml;
+};
+hipError_t launch_mla_decode(const MlaDecodeArgs& A, hipStream_t stream);
+
+// New rows into the paged latent cache.
+struct MlaAppendArgs {
+    const uint16_t* kv;          // [T] rows of kv_stride values
+    int64_t kv_stride;
+    const float* weight;         // [512] or nullptr (no norm)
+    float eps;
+    const int32_t* cu;           // [N+1] or nullptr (N sequences of equal length)
+    const int32_t* kv_lens;      // [N] rows of each sequence after the call
+    const int32_t* table;        // [N, table_width]
+    int32_t num_seqs, total, table_width;
+    uint16_t* cache;
+    int64_t page_stride;
+    int32_t num_pages, page_shift;
+};
+hipError_t launch_mla_append(const MlaAppendArgs& A, hipStream_t stream);
+
+// Verification of drafted tokens.
+constexpr int kVerifyChunk = 4096;   // tokens of the vocabulary per partial sum
+struct VerifyArgs {
+    const float* target;         // [B, D + 1] rows of target_stride values
+    const float* draft;          // [B, D] rows of draft_stride values, or nullptr
+    int64_t target_stride, draft_stride;
+    const int32_t* tokens;       // [B, D]
+    const float* uniforms;       // [B, D + 1]
+    const int32_t* num_drafts;   // [B] or nullptr
+    int32_t batch, drafts, vocab;
+    int32_t* accept;             // [B]
+    int32_t* out;                // [B, D + 1]
+    double* sums;                // workspace: [B, chunks, 2]
+};
+int32_t verify_chunks(int32_t vocab);
+hipError_t launch_verify(const VerifyArgs& A, hipStream_t stream);
+
 }  // namespace rda

@@ -26,6 +26,10 @@ RDA_HEAD_DIM = 128
 RDA_DECODE_MAX_TOKENS = 64
 RDA_GATE_SIGMOID, RDA_GATE_SILU, RDA_GATE_NONE = 0, 1, 2
 RDA_CONV_MAX_WIDTH = 4
+RDA_MLA_NOPE, RDA_MLA_PE, RDA_MLA_QK = 128, 64, 192
+RDA_MLA_V, RDA_MLA_KV = 128, 256
+RDA_MLA_LATENT, RDA_MLA_ROW = 512, 576
+RDA_MLA_MIN_PAGE, RDA_MLA_MAX_PAGE = 8, 65536
 RDA_CONV_ACT_NONE, RDA_CONV_ACT_SILU = 0, 1
 _CONV_ACTS = {"none": RDA_CONV_ACT_NONE, "silu": RDA_CONV_ACT_SILU}
 _GATE_ACTS = {"sigmoid": RDA_GATE_SIGMOID, "silu": RDA_GATE_SILU, "none": RDA_GATE_NONE}
@@ -98,6 +102,21 @@ def _load():
         lib.rda_prefill_norm_gate.argtypes = pre[:13] + [p, ctypes.c_int, p, ctypes.c_float, i32,
                                                          p, ctypes.c_int, p, p, sz, p]
         lib.rda_prefill_norm_gate.restype = ctypes.c_int
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.rda_mla_prefill.argtypes = [p, i64, p, i64, p, i64, p, p, i32, i32, i32, i32, f32,
+                                        i32, p, p, p]
+        lib.rda_mla_prefill.restype = ctypes.c_int
+        lib.rda_mla_decode_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.rda_mla_decode_workspace_bytes.restype = sz
+        lib.rda_mla_decode.argtypes = [p, p, i64, i32, i32, p, i32, p, p, i32, i32, i32, i32, f32,
+                                       p, p, p, sz, p]
+        lib.rda_mla_decode.restype = ctypes.c_int
+        lib.rda_mla_append.argtypes = [p, i64, p, f32, p, i32, i32, p, p, i32, p, i64, i32, i32, p]
+        lib.rda_mla_append.restype = ctypes.c_int
+        lib.rda_verify_drafts_workspace_bytes.argtypes = [i32, i32]
+        lib.rda_verify_drafts_workspace_bytes.restype = sz
+        lib.rda_verify_drafts.argtypes = [p, i64, p, i64, p, p, p, i32, i32, i32, p, p, p, sz, p]
+        lib.rda_verify_drafts.restype = ctypes.c_int
         lib.rda_chunk_table.argtypes = [p, i32, i32, p, p, p, p]
         lib.rda_chunk_table.restype = ctypes.c_int
         _lib = lib
@@ -394,6 +413,270 @@ def rda_decode_tokens_diag(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
     everything else as in rda_decode_tokens."""
     return _decode_tokens("rda_decode_tokens_diag", q, k, v, alpha, b, S_in, S_out, accept, o,
                           stream, True)
+
+
+def _need_gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """A tensor whose rows (all but the first axis) are contiguous; returns
+    the distance between rows in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    width, want = 1, []
+    for n in reversed(shape[1:]):
+        want.insert(0, width)
+        width *= n
+    for n, have, need in zip(shape[1:], t.stride()[1:], want):
+        if n > 1 and have != need:
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+    return t.stride(0) if shape[0] > 1 else width
+
+
+def _offsets(cu, name: str, total: int, device) -> Optional[torch.Tensor]:
+    """Packed offsets on the device: a device int32 tensor as it is (trusted,
+    like the C entry points do; no copy to the host), anything else checked
+    on the host first."""
+    if cu is None:
+        return None
+    if isinstance(cu, torch.Tensor) and cu.device == device and cu.dtype == torch.int32 \
+            and cu.is_contiguous():
+        if cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError(f"{name} must be 1-D with at least 2 entries")
+        return cu
+    return torch.from_numpy(check_cu_seqlens(cu, total)).to(device)
+
+
+def rda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float,
+                    cu_q=None, cu_k=None, *, causal: bool = True,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    want_lse: bool = False, stream=None):
+    """Expanded latent attention over packed prompts (C entry point
+    ``rda_mla_prefill``).
+
+    q [Tq, H, 192], kv [Tk, H, 256] (128 keys, then 128 values of each head),
+    k_pe [Tk, 64], all bf16, rows contiguous and any multiple of 8 elements
+    apart.  cu_q, cu_k: offsets [N+1]; a device int32 tensor is used as it is
+    (trusted, no copy to the host), anything else is checked on the host.
+    cu_k None: as cu_q.  Returns (o [Tq, H, 128] bf16, lse [Tq, H] fp32 or
+    None); lse is computed where it is passed or want_lse is set.
+    """
+    lib_ = _load()
+    dev = _need_gpu(q, "q")
+    if q.dim() != 3 or kv.dim() != 3:
+        raise ValueError("q must be [Tq, H, 192] and kv [Tk, H, 256]")
+    Tq, H, _ = q.shape
+    Tk = kv.shape[0]
+    qs = _need_rows(q, "q", torch.bfloat16, (Tq, H, RDA_MLA_QK), dev)
+    ks = _need_rows(kv, "kv", torch.bfloat16, (Tk, H, RDA_MLA_KV), dev)
+    ps = _need_rows(k_pe, "k_pe", torch.bfloat16, (Tk, RDA_MLA_PE), dev)
+    cq, ck = _offsets(cu_q, "cu_q", Tq, dev), _offsets(cu_k, "cu_k", Tk, dev)
+    if ck is not None and (cq is None or ck.numel() != cq.numel()):
+        raise ValueError("cu_k needs a cu_q of as many entries")
+    if o is None:
+        o = torch.empty((Tq, H, RDA_MLA_V), dtype=torch.bfloat16, device=dev)
+    _need(o, "o", torch.bfloat16, (Tq, H, RDA_MLA_V), dev)
+    if lse is None and want_lse:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (Tq, H), dev)
+    with torch.cuda.device(dev):
+        st = lib_.rda_mla_prefill(_ptr(q), qs, _ptr(kv), ks, _ptr(k_pe), ps, _ptr(cq), _ptr(ck),
+                                  1 if cq is None else cq.numel() - 1, Tq, Tk, H, float(scale),
+                                  int(bool(causal)), _ptr(o), _ptr(lse), _stream_handle(stream))
+    if st != 0:
+        raise RdaError(st, "rda_mla_prefill")
+    return o, lse
+
+
+def rda_mla_decode_workspace_bytes(batch: int, tokens: int, num_heads: int,
+                                   prefix_len: int = 0) -> int:
+    return int(_load().rda_mla_decode_workspace_bytes(int(batch), int(tokens), int(num_heads),
+                                                      int(prefix_len)))
+
+
+def _need_cache(cache: torch.Tensor, dev) -> int:
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be [pages, page_tokens, 576]")
+    return _need_rows(cache, "cache", torch.bfloat16,
+                      (cache.shape[0], cache.shape[1], RDA_MLA_ROW), dev)
+
+
+def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                   kv_lens: torch.Tensor, scale: float, *,
+                   prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   want_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed latent attention over a paged cache (C entry point
+    ``rda_mla_decode``).
+
+    q [B, T, H, 576] bf16, cache [pages, page_tokens, 576] bf16 (pages may be
+    further apart), block_table [B, width] int32, kv_lens [B] int32 (rows of
+    each sequence, the T new ones included), optionally prefix_table int32
+    and prefix_len: rows that the whole batch shares and sees.  All on the
+    device, never copied to the host.  Returns (o [B, T, H, 512] bf16, lse
+    [B, T, H] fp32 or None).
+    """
+    lib_ = _load()
+    dev = _need_gpu(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, H, 576]")
+    B, T, H, _ = q.shape
+    _need(q, "q", torch.bfloat16, (B, T, H, RDA_MLA_ROW), dev)
+    page_stride = _need_cache(cache, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    _need(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev)
+    _need(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    prefix_len = int(prefix_len)
+    if prefix_len > 0:
+        if prefix_table is None:
+            raise ValueError("prefix_len needs a prefix_table")
+        _need(prefix_table, "prefix_table", torch.int32, (prefix_table.numel(),), dev)
+        if prefix_table.numel() * cache.shape[1] < prefix_len:
+            raise ValueError("prefix_table holds fewer rows than prefix_len")
+    if o is None:
+        o = torch.empty((B, T, H, RDA_MLA_LATENT), dtype=torch.bfloat16, device=dev)
+    _need(o, "o", torch.bfloat16, (B, T, H, RDA_MLA_LATENT), dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, T, H), dev)
+    if workspace is None:
+        workspace = _workspace(lib_.rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)),
+                               dev, stream)
+    with torch.cuda.device(dev):
+        st = lib_.rda_mla_decode(_ptr(q), _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
+                                 _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
+                                 _ptr(prefix_table) if prefix_len > 0 else None, prefix_len, B, T,
+                                 H, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(),
+                                 _stream_handle(stream))
+    if st != 0:
+        raise RdaError(st, "rda_mla_decode")
+    return o, lse
+
+
+def _workspace(need: int, dev, stream) -> torch.Tensor:
+    """Scratch for one call, kept from reuse until the call's stream is past it."""
+    w = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        w.record_stream(stream)
+    return w
+
+
+def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                   kv_lens: torch.Tensor, cu_seqlens=None, *,
+                   weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   stream=None) -> torch.Tensor:
+    """New rows into the paged latent cache (C entry point ``rda_mla_append``).
+
+    kv [T, 576] bf16 (rows contiguous, any multiple of 8 elements apart),
+    cache, block_table and kv_lens as rda_mla_decode takes them (kv_lens: the
+    rows AFTER the call), cu_seqlens: offsets of the new tokens, as
+    rda_mla_prefill's cu_q, or None for sequences of equal length; weight
+    [512] fp32 or None (no norm).  Returns cache.
+    """
+    lib_ = _load()
+    dev = _need_gpu(kv, "kv")
+    if kv.dim() != 2:
+        raise ValueError("kv must be [T, 576]")
+    T = kv.shape[0]
+    stride = _need_rows(kv, "kv", torch.bfloat16, (T, RDA_MLA_ROW), dev)
+    page_stride = _need_cache(cache, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [N, width]")
+    N = block_table.shape[0]
+    _need(block_table, "block_table", torch.int32, (N, block_table.shape[1]), dev)
+    _need(kv_lens, "kv_lens", torch.int32, (N,), dev)
+    cu = _offsets(cu_seqlens, "cu_seqlens", T, dev)
+    if cu is not None and cu.numel() != N + 1:
+        raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (RDA_MLA_LATENT,), dev)
+    with torch.cuda.device(dev):
+        st = lib_.rda_mla_append(_ptr(kv), stride, _ptr(weight), float(eps), _ptr(cu), N, T,
+                                 _ptr(kv_lens), _ptr(block_table), block_table.shape[1],
+                                 _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
+                                 _stream_handle(stream))
+    if st != 0:
+        raise RdaError(st, "rda_mla_append")
+    return cache
+
+
+def rda_verify_drafts_workspace_bytes(batch: int, vocab: int) -> int:
+    return int(_load().rda_verify_drafts_workspace_bytes(int(batch), int(vocab)))
+
+
+def _prob_rows(t: torch.Tensor, name: str, shape, dev) -> int:
+    """[B, R, V] fp32 probabilities with equally spaced rows; their distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    B, R, V = shape
+    row = t.stride(1) if R > 1 else (t.stride(0) if B > 1 else V)
+    if (V > 1 and t.stride(2) != 1) or (B > 1 and R > 0 and t.stride(0) != R * row):
+        raise ValueError(f"{name}: rows must be contiguous and equally spaced")
+    return row
+
+
+def rda_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
+                      draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                      num_drafts: Optional[torch.Tensor] = None, *,
+                      accept: Optional[torch.Tensor] = None,
+                      out_tokens: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Verification of drafted tokens (C entry point ``rda_verify_drafts``).
+
+    target [B, D+1, V] fp32 probabilities, draft [B, D, V] fp32 or None
+    (drafts without probabilities), draft_tokens [B, D] int32, uniforms
+    [B, D+1] fp32, num_drafts [B] int32 or None.  Returns (accept [B] int32,
+    the accept counts that rda_decode_tokens takes, out_tokens [B, D+1] int32).
+    """
+    lib_ = _load()
+    dev = _need_gpu(target, "target")
+    if target.dim() != 3 or target.shape[1] < 1:
+        raise ValueError("target must be [B, D+1, V]")
+    B, T, V = target.shape
+    ts = _prob_rows(target, "target", (B, T, V), dev)
+    ds = _prob_rows(draft, "draft", (B, T - 1, V), dev) if draft is not None else 0
+    _need(draft_tokens, "draft_tokens", torch.int32, (B, T - 1), dev)
+    _need(uniforms, "uniforms", torch.float32, (B, T), dev)
+    if num_drafts is not None:
+        _need(num_drafts, "num_drafts", torch.int32, (B,), dev)
+    if accept is None:
+        accept = torch.empty((B,), dtype=torch.int32, device=dev)
+    _need(accept, "accept", torch.int32, (B,), dev)
+    if out_tokens is None:
+        out_tokens = torch.empty((B, T), dtype=torch.int32, device=dev)
+    _need(out_tokens, "out_tokens", torch.int32, (B, T), dev)
+    if workspace is None:
+        workspace = _workspace(lib_.rda_verify_drafts_workspace_bytes(B, V), dev, stream)
+    with torch.cuda.device(dev):
+        st = lib_.rda_verify_drafts(_ptr(target), ts, _ptr(draft) if T > 1 else None, ds,
+                                    _ptr(draft_tokens), _ptr(uniforms), _ptr(num_drafts), B, T - 1,
+                                    V, _ptr(accept), _ptr(out_tokens), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream_handle(stream))
+    if st != 0:
+        raise RdaError(st, "rda_verify_drafts")
+    return accept, out_tokens
 
 
 def rda_chunk_table(cu_seqlens, num_seqs: int, total_tokens: int, device="cuda",

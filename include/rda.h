@@ -63,6 +63,16 @@ extern "C" {
 #define RDA_HEAD_DIM 128  /* the only supported dk = dv */
 #define RDA_DECODE_MAX_TOKENS 64  /* tokens per rda_decode_tokens call (one chunk) */
 #define RDA_CONV_MAX_WIDTH 4      /* taps of the prologue's short convolution */
+/* Widths of the latent attention (the hybrid's layers beside RDA) */
+#define RDA_MLA_NOPE 128    /* a head's own query / key channels */
+#define RDA_MLA_PE 64       /* key channels that the heads share */
+#define RDA_MLA_QK 192      /* query width of a head, expanded form: NOPE + PE */
+#define RDA_MLA_V 128       /* value channels of a head */
+#define RDA_MLA_KV 256      /* expanded keys and values of a head: NOPE + V */
+#define RDA_MLA_LATENT 512  /* the latent vector */
+#define RDA_MLA_ROW 576     /* a cached row, and an absorbed query: LATENT + PE */
+#define RDA_MLA_MIN_PAGE 8       /* rows of a cache page: a power of two */
+#define RDA_MLA_MAX_PAGE 65536
 
 typedef enum {
     RDA_OK = 0,
@@ -467,6 +477,163 @@ rda_status rda_prefill_norm_gate(const void* q, const void* k, const void* v, rd
                                  const float* weight, float eps, int32_t act, void* out,
                                  rda_dtype out_dtype, float* S_final, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Latent attention: the attention of the hybrid's other layers (the Raon-1
+ * nano teardown and the "Raon-1-nano-gguf" card's spec table: every fourth
+ * layer, 32 heads, 192 QK / 128 V channels, no position encoding; the
+ * teardown's section "The cache is small if the runtime keeps it small"
+ * counts its cache at 576 values per token and layer).  All keys and values
+ * of a token come from one latent vector c of 512 values and 64 key channels
+ * shared by the heads: k = (W_k c, pe), v = W_v c per head.
+ *
+ * Shared by the three entry points below: values are bf16; products, softmax
+ * statistics and sums are fp32; probabilities are rounded to bf16 for the
+ * second product, the output once at its end.  int32 arrays and lse need
+ * 4-byte alignment only.  Key rows that a query does not see do not reach its
+ * output, whatever they hold (infinities and NaN included).  A query that
+ * sees no key gets o = 0 and lse = -inf.
+ *
+ * rda_mla_prefill is the expanded form over packed prompts:
+ *
+ *     s_ij = scale (q_i[0:128] . kn_j + q_i[128:192] . pe_j)
+ *     o_i  = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
+ *
+ * over the keys j of the query's sequence, with causal = 1 only those with
+ * j <= i + (keys - queries): the queries are the sequence's last tokens, the
+ * keys before them what is cached of it.
+ *
+ *   q       [total_q] rows q_stride values apart, head h at 192 h
+ *   kv      [total_k] rows kv_stride values apart, head h's 128 keys and 128
+ *           values at 256 h (the up-projection's output as it is)
+ *   k_pe    [total_k] rows pe_stride values apart of 64 values (a slice of
+ *           the cached rows as it is)
+ *           Strides are multiples of 8, at least the row's width and at most
+ *           2^24 (RDA_ERR_SHAPE).
+ *   cu_q, cu_k  device int32 [num_seqs + 1] offsets of the queries and keys
+ *           (trusted as in rda_prefill, never used out of bounds); cu_k NULL:
+ *           as cu_q (total_k = total_q); both NULL: one sequence
+ *   scale   finite and > 0; causal 0 or 1 (RDA_ERR_VALUE)
+ *   o       [total_q, H, 128] bf16; lse [total_q, H] fp32 or NULL.  Neither
+ *           may overlap an input or the other (RDA_ERR_ALIAS).
+ */
+rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int64_t kv_stride,
+                           const void* k_pe, int64_t pe_stride, const int32_t* cu_q,
+                           const int32_t* cu_k, int32_t num_seqs, int32_t total_q,
+                           int32_t total_k, int32_t num_heads, float scale, int32_t causal,
+                           void* o, float* lse, hipStream_t stream);
+
+/* Workspace bytes rda_mla_decode needs (0 on bad sizes).  Its contents need
+ * no initialisation; two calls that may overlap in time need one each. */
+size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
+                                      int32_t prefix_len);
+
+/*
+ * The absorbed form, for decoding: a head's query arrives multiplied by W_k
+ * (512 values, then its 64 for the shared channels) and meets the cached rows
+ * themselves, s_ij = scale q_i . c_j, o_i = sum_j exp(s_ij - lse_i) c_j[0:512],
+ * which W_v takes to the head's values afterwards.  `tokens` new tokens per
+ * sequence (one, or a current token and its drafts, as in rda_decode_tokens),
+ * whose rows are the last of the kv_lens[b] cached ones (rda_mla_append comes
+ * first): token t sees the sequence's rows j < kv_lens[b] - (tokens - 1 - t).
+ *
+ * Optionally the batch shares a prefix (a common prompt): prefix_len rows in
+ * the pages of prefix_table, before every sequence's own rows and seen by
+ * every query.  They are read once for all the batch's queries, as one
+ * product; kv_lens and block_table then count only a sequence's own rows.
+ *
+ *   q           [batch, tokens, H, 576] bf16
+ *   cache       num_pages pages, page_stride values apart (a multiple of 8),
+ *               of page_tokens contiguous rows of 576 bf16 values;
+ *               page_tokens a power of two in [RDA_MLA_MIN_PAGE,
+ *               RDA_MLA_MAX_PAGE] (RDA_ERR_UNSUPPORTED)
+ *   block_table device int32 [batch, table_width]: the pages of a sequence's
+ *               rows in order; entries behind its last page are not read
+ *   kv_lens     device int32 [batch]; clamped to [0, table_width x
+ *               page_tokens].  Page ids are trusted, but never used out of
+ *               bounds (an id outside [0, num_pages) reads some page)
+ *   prefix_table  device int32 [ceil(prefix_len / page_tokens)], not read
+ *               where prefix_len = 0
+ *   tokens in [0, RDA_DECODE_MAX_TOKENS]; scale finite and > 0
+ *   o           [batch, tokens, H, 512] bf16; lse [batch, tokens, H] fp32 or
+ *               NULL
+ * The lengths are read on the device: a captured call may be replayed with
+ * other lengths and tables.  For the same lengths results are the same bit
+ * for bit.
+ */
+rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
+                          int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                          const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
+                          int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * New rows into the cache that rda_mla_decode reads: the latent projection's
+ * output, with the latent part RMS-normalised as the model's kv norm does,
+ *
+ *     y_c = x_c / sqrt(mean_{c' < 512} x_c'^2 + eps) * weight_c   (c < 512),
+ *
+ * rounded to bf16, and the 64 shared key channels as they are.
+ *
+ *   kv          [total_tokens] rows kv_stride values apart of 576 bf16 values
+ *   weight      [512] fp32, or NULL to copy the latent part as it is
+ *   eps         finite and >= 0 (RDA_ERR_VALUE)
+ *   cu_seqlens  device int32 [num_seqs + 1] offsets of the new tokens, or
+ *               NULL for num_seqs sequences of equal length
+ *   kv_lens     device int32 [num_seqs]: rows of each sequence AFTER the call
+ *               (what rda_mla_decode takes); sequence n's new rows go to the
+ *               positions before kv_lens[n]
+ *   block_table, cache, page_stride, num_pages, page_tokens
+ *               as in rda_mla_decode.  A row whose position or page id is out
+ *               of range is not written; nothing else of the cache changes.
+ * Two positions that share a page slot (a page listed twice) leave one of
+ * the two rows there.
+ */
+rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight, float eps,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                          const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
+                          void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                          hipStream_t stream);
+
+/* Workspace bytes rda_verify_drafts needs (0 on bad sizes); no
+ * initialisation, one per call that may overlap another. */
+size_t rda_verify_drafts_workspace_bytes(int32_t batch, int32_t vocab);
+
+/*
+ * Verification of drafted tokens: which of them stand, and the token after
+ * them, distributed as the target model's own.  With u the given random
+ * numbers in [0, 1), draft i of a sequence is accepted while
+ *
+ *     u_i q_i(d_i) < p_i(d_i);
+ *
+ * with r accepted, the next token is the smallest j with
+ * sum_{j' <= j} w_j' > u_D sum_j' w_j' (D = drafts), where w = max(p_r - q_r, 0) if draft r
+ * was refused and w = p_r if none was (or if that leaves nothing).
+ *
+ *   target        [batch, drafts + 1] rows target_stride values apart of
+ *                 `vocab` fp32 probabilities: after the current token and
+ *                 after each draft.  They need not sum to 1; what is not a
+ *                 positive finite number weighs nothing
+ *   draft         [batch, drafts] rows draft_stride values apart of the
+ *                 probabilities the drafts were drawn from, or NULL for
+ *                 drafts without any (q_i = 1 at d_i and 0 elsewhere)
+ *   draft_tokens  device int32 [batch, drafts]; one outside [0, vocab) is
+ *                 refused
+ *   uniforms      [batch, drafts + 1] fp32, independent: one per draft, and the
+ *                 last for the next token
+ *   num_drafts    device int32 [batch], clamped to [0, drafts], or NULL: all
+ *   accept        [batch] int32: 1 + r, the accept counts of
+ *                 rda_decode_tokens over the current token and the drafts
+ *   out_tokens    [batch, drafts + 1] int32: the accepted drafts, the next
+ *                 token (-1 if no token weighs anything), then -1
+ * drafts in [0, RDA_DECODE_MAX_TOKENS - 1]; batch at most 65535.  Products
+ * and sums are in 64 bits.  Outputs may not overlap anything.
+ */
+rda_status rda_verify_drafts(const float* target, int64_t target_stride, const float* draft,
+                             int64_t draft_stride, const int32_t* draft_tokens,
+                             const float* uniforms, const int32_t* num_drafts, int32_t batch,
+                             int32_t drafts, int32_t vocab, int32_t* accept, int32_t* out_tokens,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Test hook: the chunk table rda_prefill builds from cu_seqlens.
