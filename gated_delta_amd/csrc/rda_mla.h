@@ -39,8 +39,12 @@ __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t x) {
     return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
-__device__ __forceinline__ bool nonfinite(float x) {
-    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+// Infinities and NaN to zero.
+__device__ __forceinline__ bf16x8 finite_only(bf16x8 x) {
+    u32x4 v = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] &= ~((nonfinite_bits(v[i]) >> 15) * 0xffffu);
+    return __builtin_bit_cast(bf16x8, v);
 }
 
 // 8 consecutive accumulator registers as one bf16 MFMA operand.
@@ -74,6 +78,13 @@ __device__ __forceinline__ void dma16_from(const void* p, uint32_t lds) {
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return uint32_t(reinterpret_cast<uintptr_t>((lds_void*)p));
+}
+
+// x, computed anew where this stands: what follows from it is not kept in
+// registers across a loop around it.
+__device__ __forceinline__ int here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;

@@ -30,46 +30,60 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 32;                          // cached rows per tile
 constexpr int kRowBytes = kMlaRow * 2;             // 1152
+constexpr int kLatBytes = kMlaLatent * 2, kPeBytes = kMlaPe * 2;
 constexpr int kTileBytes = kTile * kRowBytes;      // 36864
 constexpr int kGroups = kMlaLatent / 4;            // 4-channel groups of an output row
 
 typedef const __attribute__((address_space(4))) int32_t const_i32;
 
-__device__ const __attribute__((aligned(16))) uint32_t kZeros[4] = {0, 0, 0, 0};
+// What rows behind the last one are read as.
+__device__ const __attribute__((aligned(16))) uint32_t kZeros[kLatBytes / 4] = {};
 
-// Row r of a tile keeps 16-byte granule j (0..71) at j ^ swizzle(r), inside
-// groups of eight.  Rows are 72 granules apart, 8 modulo 16, so bit 0 of r
-// already parts the banks; bits 1..3 go to granule bits 1, 2, 0: sixteen
-// rows at one granule, and eight rows at two adjacent ones (transposing
-// reads), fall on distinct banks.
-__device__ __forceinline__ int row_swz(int r) {
-    return (r & 2) | (r & 4) | ((r >> 3) & 1);
-}
+// A tile keeps its rows' latent parts (64 granules of 16 bytes each, granule
+// j of row r at j ^ swz(r)), then their shared key channels (8 granules, j at
+// j ^ (r >> 1 & 7)): sixteen rows read at one granule, and eight rows at two
+// adjacent ones (transposing reads), fall on distinct banks.
+struct Tile {
+    unsigned char lat[kTile * kLatBytes];
+    unsigned char pe[kTile * kPeBytes];
+};
 
 struct Lds {
-    unsigned char tile[4][kTileBytes];
+    Tile tile[4];
     float ml[4][2][32];     // (mu, l) of each wave's rows
     int scan[8];
     int unit, first;        // where this workgroup's piece begins
 };
 
-// LDS byte offsets (from a tile's start) of this lane's operands.
+// LDS byte offsets of this lane's operands, from a tile's start: the others
+// differ by exclusive-or of granule bits and by constants.
 struct Addr {
-    uint32_t k[4], v[2][2];
+    int k, pe, v;
+    __device__ __forceinline__ Addr(int k_, int pe_, int v_) : k(k_), pe(pe_), v(v_) {}
     __device__ __forceinline__ explicit Addr(int l) {
         const int r = l & 31, g = l >> 5, j = l & 15;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) k[m] = r * kRowBytes + 16 * ((2 * m + g) ^ row_swz(r));
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-            const int vr = 4 * g + 8 * hi + (j >> 2);
-            const int low = 2 * ((l >> 4) & 1) + ((j >> 1) & 1);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                v[b][hi] = vr * kRowBytes + 16 * ((4 * b + low) ^ row_swz(vr)) + 8 * (j & 1);
-        }
+        k = r * kLatBytes + 16 * (g ^ swz(r));
+        pe = kTile * kLatBytes + r * kPeBytes + 16 * (g ^ ((r >> 1) & 7));
+        // C^T operand: channel l % 32, rows 4g + {0..3}
+        const int vr = 4 * g + (j >> 2), low = 2 * ((l >> 4) & 1) + ((j >> 1) & 1);
+        v = vr * kLatBytes + 16 * (low ^ swz(vr)) + 8 * (j & 1);
     }
 };
+
+// Row operand of the tile at LDS address `tile`: values 16 m + 8 g ..
+__device__ __forceinline__ bf16x8 k_op(const Addr& a, uint32_t tile, int m) {
+    return lds_read16(m < 32 ? tile + (a.k ^ (32 * (m & 7))) + 256 * (m >> 3)
+                             : tile + (a.pe ^ (32 * (m & 3))));
+}
+
+// C^T operand: channel block b, rows 16 k + 4g + {0..3, 8..11} (rows eight
+// further on have the other lowest bit in their swizzle).
+__device__ __forceinline__ bf16x8 v_op(const Addr& a, uint32_t tile, int b, int k) {
+    const uint32_t at = 256 * (b >> 2) + k * 16 * kLatBytes;
+    const u32x2 x = lds_read_tr8(tile + (a.v ^ (64 * (b & 3))) + at);
+    const u32x2 y = lds_read_tr8(tile + (a.v ^ (64 * (b & 3) + 16)) + 8 * kLatBytes + at);
+    return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+}
 
 __device__ __forceinline__ int clamp_len(const MlaDecodeArgs& A, int b) {
     const int64_t most = int64_t(A.table_width) << A.page_shift;
@@ -83,6 +97,8 @@ struct Source {
     int len;
 };
 
+// (table through the constant address space: a scalar load where k is uniform,
+// which no wait for transfers in flight stands in the way of)
 __device__ __forceinline__ const uint16_t* cached_row(const MlaDecodeArgs& A, const int32_t* table,
                                                       int k) {
     const int page = min(max(((const_i32*)table)[k >> A.page_shift], 0), A.num_pages - 1);
@@ -90,60 +106,39 @@ __device__ __forceinline__ const uint16_t* cached_row(const MlaDecodeArgs& A, co
            int64_t(k & ((1 << A.page_shift) - 1)) * kMlaRow;
 }
 
-// Eight rows [k, k + 8) of a tile: 9 transfers of 1 KiB.  Lane offsets within
-// eight rows are in `off`; a tile's odd groups of eight flip granule bit 0.
-// A page holds whole groups of eight.
+// Eight rows [k, k + 8) of a tile (its rows 8 group ..): a transfer of 1 KiB
+// per latent part, one for the eight rows' shared channels.  A page holds
+// whole groups of eight.
 __device__ __forceinline__ void issue8(const MlaDecodeArgs& A, const Source& src, int k, int group,
-                                       const uint32_t (&off)[9], int l, uint32_t lds) {
-    const uint32_t flip = 16 * (group & 1);
-    lds += group * 8 * kRowBytes;
+                                       int lane_id, uint32_t lds) {
+    const int l = here(lane_id);
+    const char* base = reinterpret_cast<const char*>(
+        k < src.len ? cached_row(A, src.table, k) : A.cache);
+    const uint32_t lat = lds + group * 8 * kLatBytes;
+    const uint32_t pe = lds + kTile * kLatBytes + group * 8 * kPeBytes;
+    const int pr = l >> 3, pj = (l & 7) ^ ((4 * group + (pr >> 1)) & 7);
+    const uint32_t pe_off = pr * kRowBytes + kLatBytes + 16 * pj;
+    const uint32_t lane = 16 * (l ^ (group & 1));
     if (k + 8 <= src.len) {
-        const uint16_t* base = cached_row(A, src.table, k);
 #pragma unroll
-        for (int i = 0; i < 9; ++i) dma16_at(base, off[i] ^ flip, lds + 1024 * i);
+        for (int r = 0; r < 8; ++r) dma16_at(base + r * kRowBytes, lane ^ (32 * r), lat + r * kLatBytes);
+        dma16_at(base, pe_off, pe);
     } else {   // rows behind the last one are zeros
-        const uint16_t* base = k < src.len ? cached_row(A, src.table, k) : A.cache;
 #pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            const int r = (64 * i + l) / 72;
-            const char* p = k + r < src.len
-                ? reinterpret_cast<const char*>(base) + (off[i] ^ flip)
-                : reinterpret_cast<const char*>(kZeros);
-            dma16_from(p, lds + 1024 * i);
-        }
+        for (int r = 0; r < 8; ++r)
+            dma16_at(k + r < src.len ? base + r * kRowBytes : reinterpret_cast<const char*>(kZeros),
+                     lane ^ (32 * r), lat + r * kLatBytes);
+        dma16_from(k + pr < src.len ? base + pe_off : reinterpret_cast<const char*>(kZeros), pe);
     }
 }
 
-// The values of masked tiles with infinities or NaN among the rows that some
-// queries do not see: added row by row, to the queries that see them.
-__device__ __forceinline__ void add_masked_values(const MlaDecodeArgs& A, const int32_t* table,
-                                                  const uint16_t* qrow, int from, int limit,
-                                                  float c, float mu, int g, int ch0, f32x16 (&acc)[8]) {
-    for (int k = from; k < limit; ++k) {
-        const int page = min(max(table[k >> A.page_shift], 0), A.num_pages - 1);
-        const uint16_t* row = A.cache + int64_t(page) * A.page_stride +
-                              int64_t(k & ((1 << A.page_shift) - 1)) * kMlaRow;
-        float s = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < kMlaRow; ++d)
-            s = fmaf(bf16_bits_to_f32(qrow[d]), bf16_bits_to_f32(row[d]), s);
-        const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -mu));
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                acc[b][i] = fmaf(p, bf16_bits_to_f32(row[ch0 + 32 * b + d_row(i, g)]), acc[b][i]);
+// Infinities and NaN in the latent parts of `n` groups of eight rows to zero.
+__device__ __forceinline__ void clean_rows(uint32_t tile, int group, int n, int l) {
+    typedef __attribute__((address_space(3))) u32x4 lds_quad;
+    for (int r = 0; r < 8 * n; ++r) {
+        lds_quad* p = (lds_quad*)(lds_char*)uintptr_t(tile + (8 * group + r) * kLatBytes + 16 * l);
+        *p = __builtin_bit_cast(u32x4, finite_only(__builtin_bit_cast(bf16x8, *p)));
     }
-}
-
-// Latent values of the tile's rows [from, 32) (within the tile) not finite?
-__device__ __forceinline__ bool rows_nonfinite(const unsigned char* tile, int from, int l) {
-    uint32_t bad = 0;
-    for (int r = max(from, 0); r < kTile; ++r) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + r * kRowBytes + 16 * l);
-        bad |= nonfinite_bits(x[0]) | nonfinite_bits(x[1]) | nonfinite_bits(x[2]) | nonfinite_bits(x[3]);
-    }
-    return __any(bad != 0);
 }
 
 // Where a piece's sums go: the outputs, or a slot of partial sums.
@@ -182,11 +177,94 @@ __device__ __forceinline__ void put_ml(const MlaDecodeArgs& A, const Sink& S, in
 
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// x * a with x kept in an accumulation register on every path: written plainly
+// the compiler holds the sums in ordinary registers between the tiles and
+// moves all of them twice per tile.  (x's last product is a tile ago, so no
+// wait for the matrix core stands here.)
+__device__ __forceinline__ float scale_acc(float x, float a) {
+    float t;
+    asm("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %2, %1\n\tv_accvgpr_write_b32 %0, %1"
+        : "+a"(x), "=&v"(t)
+        : "v"(a));
+    return x;
+}
+
+// A sum out of its accumulation register (see scale_acc); settle() first.
+__device__ __forceinline__ float read_acc(float x) {
+    float y;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(y) : "a"(x));
+    return y;
+}
+
+__device__ __forceinline__ f32x4 read_acc4(const f32x16& x, int r) {
+    return f32x4{read_acc(x[r]), read_acc(x[r + 1]), read_acc(x[r + 2]), read_acc(x[r + 3])};
+}
+
+// Longer than the last matrix products take to write their registers.
+__device__ __forceinline__ void settle() {
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15");
+}
+
+// A piece's sums to where they go; with two pairs, joined first.
+template <int kRG>
+__device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const Sink& sink,
+                                       const f32x16 (&acc)[8], float mu, float lsum) {
+    constexpr int kKW = 2 / kRG;
+    const int w = wave_id(), l = here(threadIdx.x & 63), g = l >> 5;
+    const int half = w & 1, rg = kRG == 2 ? w >> 1 : 0, kw = kRG == 2 ? 0 : w >> 1;
+    const int row = 32 * rg + (l & 31);
+    settle();
+    if constexpr (kKW == 1) {
+        const float inv = inverse(lsum);
+        if (g == 0 && half == 0) put_ml(A, sink, row, mu, lsum);
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                put4(A, sink, row, 256 * half + 32 * b + d_row(r, g),
+                     read_acc4(acc[b], r), inv);
+    } else {
+        // the two pairs' sums meet in LDS; each wave joins half of its channels
+        raw_barrier();   // the tiles are read
+        if (g == 0) {
+            lds.ml[w][0][l] = mu;
+            lds.ml[w][1][l] = lsum;
+        }
+        f32x4* mine = reinterpret_cast<f32x4*>(&lds.tile[w]);
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                mine[(b * 4 + r / 4) * 64 + l] = read_acc4(acc[b], r);
+        raw_barrier();
+        float f[2], total = 0.f, top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) top = fmaxf(top, lds.ml[2 * k + half][0][l & 31]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float x = lds.ml[2 * k + half][0][l & 31];
+            f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
+            total = fmaf(lds.ml[2 * k + half][1][l & 31], f[k], total);
+        }
+        if (w == 0 && g == 0) put_ml(A, sink, row, top, total);
+        const float inv = inverse(total);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int blk = 4 * kw + b;
+                const f32x4 x = reinterpret_cast<const f32x4*>(&lds.tile[half])[(blk * 4 + r) * 64 + l];
+                const f32x4 y = reinterpret_cast<const f32x4*>(&lds.tile[2 + half])[(blk * 4 + r) * 64 + l];
+                put4(A, sink, row, 256 * half + 32 * blk + d_row(4 * r, g), x * f[0] + y * f[1], inv);
+            }
+    }
+    raw_barrier();   // the next piece refills the tiles
+}
+
 // One piece: tiles [t0, t1) of a source for 32 kRG query rows.
 template <int kRG, bool kCausal>
-__device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Addr& addr,
-                                      const uint32_t (&off)[9], const Source& src, int t0, int t1,
-                                      const Sink& sink) {
+__device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Addr& addr0,
+                                      const Source& src, int t0, int t1, const Sink& sink) {
     constexpr int kKW = 2 / kRG;        // pairs that take tiles in turn
     constexpr int kBuf = 2 * kRG;       // tile buffers of such a pair (or of both)
     constexpr int kIssue = 2 / kRG;     // groups of eight rows that a wave fetches
@@ -204,17 +282,16 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
     const float c = A.scale * kLog2e;
     float m = -INFINITY, mu = 0.f, lsum = 0.f;
     f32x16 acc[8] = {};
-    int left_from = -1;   // first row of the tiles left to add_masked_values
 #pragma unroll
     for (int i = 0; i < 36; ++i) asm volatile("" : "+v"(qf[i]));
 
-    const uint32_t group_lds = lds_addr(lds.tile[kw * kBuf]);
+    const uint32_t group_lds = lds_addr(&lds.tile[kw * kBuf]);
     const int share = kRG == 2 ? w : half;   // this wave's part of a tile
     auto issue = [&](int t, int buf) {
 #pragma unroll
         for (int i = 0; i < kIssue; ++i) {
             const int group = share * kIssue + i;
-            issue8(A, src, t * kTile + 8 * group, group, off, l, group_lds + buf * kTileBytes);
+            issue8(A, src, t * kTile + 8 * group, group, l, group_lds + buf * kTileBytes);
         }
     };
     const int steps = (t1 - t0 + kKW - 1) / kKW;
@@ -223,7 +300,8 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
         const int t = t0 + d * kKW + kw;
         if (t < t1) issue(t, d);
     }
-    for (int i = 0; i < steps; ++i) {
+    const int own = (t1 - t0 - kw + kKW - 1) / kKW;   // the other pair may have one more
+    for (int i = 0; i < own; ++i) {
         const int t = t0 + i * kKW + kw, buf = i % kBuf;
         // this wave's part of tile i has landed once only later tiles' parts
         // are on their way
@@ -233,13 +311,18 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
         raw_barrier();   // everyone's part has, and tile i - 1 is read
         const int next = t + (kBuf - 1) * kKW;
         if (next < t1) issue(next, (i + kBuf - 1) % kBuf);
-        if (t >= t1) continue;
+        // several new tokens: 0 * inf from a row that only later ones see would
+        // reach the earlier ones, so the last tiles' latent values are made
+        // finite before they serve as values (the combine kernel sets the
+        // outputs of the queries that do see such a row)
+        const bool cleaned = kCausal && A.tokens > 1 && (t0 + (i + 1) * kKW) * kTile > all_see;
         const uint32_t base = group_lds + buf * kTileBytes;
         const int k0 = t * kTile;
+        const Addr addr{here(addr0.k), here(addr0.pe), here(addr0.v)};
         f32x16 s = {};
 #pragma unroll
         for (int mm = 0; mm < 36; ++mm)
-            s = mfma32(lds_read16(base + addr.k[mm & 3] + 128 * (mm >> 2)), qf[mm], s);
+            s = mfma32(k_op(addr, base, mm), qf[mm], s);
         const bool masked = k0 + kTile > all_see;
         if (masked) {
 #pragma unroll
@@ -259,9 +342,10 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
             mu = mun;
             lsum *= a;
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
+            for (int b = 0; b < 8; ++b) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[b][r] *= a;
+                for (int r = 0; r < 16; ++r) acc[b][r] = scale_acc(acc[b][r], a);
+            }
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -269,85 +353,28 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
             lsum += s[r];
         }
         const bf16x8 p[2] = {pack8<0>(s), pack8<8>(s)};
-        if (kCausal && masked && (left_from >= 0 ||
-                       rows_nonfinite(lds.tile[kw * kBuf + buf], all_see - k0, l))) {
-            if (left_from < 0) left_from = k0;
-        } else {
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a = base + 512 * half + 128 * (b >> 1) + k * 16 * kRowBytes;
-                    const u32x2 x = lds_read_tr8(a + addr.v[b & 1][0]);
-                    const u32x2 y = lds_read_tr8(a + addr.v[b & 1][1]);
-                    acc[b] = mfma32(__builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]}), p[k],
-                                    acc[b]);
-                }
+        if (cleaned) {
+            raw_barrier();
+            clean_rows(group_lds + buf * kTileBytes, share * kIssue, kIssue, l);
+            raw_barrier();
         }
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                acc[b] = mfma32(v_op(addr, base + 512 * half, b, k), p[k], acc[b]);
     }
-    if (kCausal && left_from >= 0) {
-        // (the other pair's tiles are not this one's)
-        for (int k0 = left_from; k0 < t1 * kTile; k0 += kTile * kKW)
-            add_masked_values(A, src.table, qrow, k0, min(limit, k0 + kTile), c, mu, g, 256 * half, acc);
+    if (kKW > 1 && own < steps) {
+        raw_barrier();
+        if (kCausal && A.tokens > 1 && (t0 + steps * kKW) * kTile > all_see) {
+            raw_barrier();
+            raw_barrier();
+        }
     }
     lsum += other_half(lsum);
     mu = m == -INFINITY ? -INFINITY : mu;
 
-    if constexpr (kKW == 1) {
-        const float inv = inverse(lsum);
-        if (g == 0 && half == 0) put_ml(A, sink, row, mu, lsum);
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                put4(A, sink, row, 256 * half + 32 * b + d_row(r, g),
-                     f32x4{acc[b][r], acc[b][r + 1], acc[b][r + 2], acc[b][r + 3]}, inv);
-    } else {
-        // the two pairs' sums meet in LDS; each wave joins half of its channels
-        raw_barrier();   // the tiles are read
-        if (g == 0) {
-            lds.ml[w][0][l] = mu;
-            lds.ml[w][1][l] = lsum;
-        }
-        f32x4* mine = reinterpret_cast<f32x4*>(lds.tile[w]);
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                mine[(b * 4 + r / 4) * 64 + l] =
-                    f32x4{acc[b][r], acc[b][r + 1], acc[b][r + 2], acc[b][r + 3]};
-        raw_barrier();
-        float f[2], total = 0.f, top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) top = fmaxf(top, lds.ml[2 * k + half][0][l & 31]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float x = lds.ml[2 * k + half][0][l & 31];
-            f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
-            total = fmaf(lds.ml[2 * k + half][1][l & 31], f[k], total);
-        }
-        if (w == 0 && g == 0) put_ml(A, sink, row, top, total);
-        const float inv = inverse(total);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int blk = 4 * kw + b;
-                const f32x4 x = reinterpret_cast<const f32x4*>(lds.tile[half])[(blk * 4 + r) * 64 + l];
-                const f32x4 y = reinterpret_cast<const f32x4*>(lds.tile[2 + half])[(blk * 4 + r) * 64 + l];
-                put4(A, sink, row, 256 * half + 32 * blk + d_row(4 * r, g), x * f[0] + y * f[1], inv);
-            }
-    }
-    raw_barrier();   // the next piece refills the tiles
-}
-
-// Lane offsets of nine transfers over eight rows, from the first of them.
-__device__ __forceinline__ void lane_offsets(int l, uint32_t (&off)[9]) {
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-        const int G = 64 * i + l, r = G / 72, pos = G - 72 * r;
-        off[i] = r * kRowBytes + 16 * (pos ^ row_swz(r));
-    }
+    finish<kRG>(A, lds, sink, acc, mu, lsum);
 }
 
 // A value that every lane holds alike, in scalar registers.
@@ -417,8 +444,6 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     int first = __builtin_amdgcn_readfirstlane(lds.first);
 
     const Addr addr(l);
-    uint32_t off[9];
-    lane_offsets(l, off);
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
     int64_t at = begin;
     while (at < end) {
@@ -446,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
             A.meta[2 * unit] = sink.final ? -1 : wg;
             A.meta[2 * unit + 1] = int((stop - 1) / per);
         }
-        piece<kRG, true>(A, lds, addr, off, Source{A.table + int64_t(b) * A.table_width, len}, first,
+        piece<kRG, true>(A, lds, addr, Source{A.table + int64_t(b) * A.table_width, len}, first,
                          last, sink);
         at += last - first;
         first = 0;
@@ -460,8 +485,6 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
     __shared__ __attribute__((aligned(256))) Lds lds;
     const int l = threadIdx.x & 63, wg = blockIdx.x;
     const Addr addr(l);
-    uint32_t off[9];
-    lane_offsets(l, off);
     const int64_t rows = int64_t(A.batch) * A.tokens * A.heads;
     const int n = tiles_of(A.prefix_len);
     const int64_t total = int64_t(A.prefix_units) * n;
@@ -479,24 +502,61 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
         sink.part = A.pre_part + size_t(slot) * kGroups * 4 * 32 * kRG;
         sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRG;
         sink.stride = 32 * kRG;
-        piece<kRG, false>(A, lds, addr, off, Source{A.prefix_table, A.prefix_len}, first, last, sink);
+        piece<kRG, false>(A, lds, addr, Source{A.prefix_table, A.prefix_len}, first, last, sink);
         at += last - first;
     }
 }
 
 // Joins the partial sums of 32 query rows of a unit, 64 channels a workgroup.
+// Where there are several new tokens it also looks at the rows of the tiles
+// that some of them do not see: a latent value that is infinite or NaN makes
+// that channel NaN for the queries that see it (its score is infinite or NaN
+// too), and the products left it out.
 __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeArgs A) {
+    __shared__ int bad_s;
     const int unit = blockIdx.x / A.row_groups, sub = blockIdx.x % A.row_groups;
     const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
     const int stride = 32 * A.row_groups;
     const int lr = 32 * sub + int(threadIdx.x & 31);     // row in the unit's block
     const int urow = stride * blk + lr;                  // row in the sequence
-    const bool any = clamp_len(A, b) > 0;
+    const int len = clamp_len(A, b);
+    const bool any = len > 0;
     const int g0 = any ? A.meta[2 * unit] : -1, g1 = any ? A.meta[2 * unit + 1] : -2;
-    if (any && g0 < 0) return;                           // already written
-    if (urow >= unit_rows) return;
+    const int32_t* table = A.table + int64_t(b) * A.table_width;
+    const int from = max(len - (A.tokens - 1), 0) / kTile * kTile;
+    const int cg0 = blockIdx.y * 16 + 2 * int(threadIdx.x >> 5);
+    bool bad = false;
+    if (A.tokens > 1) {
+        for (int k = from + int(threadIdx.x >> 3); k < len; k += kThreads / 8) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(
+                cached_row(A, table, k) + 64 * blockIdx.y + 8 * (threadIdx.x & 7));
+            bad |= (nonfinite_bits(x[0]) | nonfinite_bits(x[1]) | nonfinite_bits(x[2]) |
+                    nonfinite_bits(x[3])) != 0;
+        }
+        if (threadIdx.x == 0) bad_s = 0;
+        __syncthreads();
+        if (bad) bad_s = 1;
+        __syncthreads();
+        bad = bad_s != 0;
+    }
+    const bool done = any && g0 < 0;                     // already written
+    if (urow >= unit_rows || (done && !bad)) return;
+    u32x4 nan = {};                                      // 0xffff where a channel is NaN
+    if (bad) {
+        const int limit = len - (A.tokens - 1 - urow / A.heads);
+        for (int k = from; k < limit; ++k) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(cached_row(A, table, k) + 4 * cg0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nan[i] |= (nonfinite_bits(x[i]) >> 15) * 0xffffu;
+        }
+    }
     const int64_t row = int64_t(b) * unit_rows + urow;
+    u32x4* const o = reinterpret_cast<u32x4*>(A.o + row * kMlaLatent + 4 * cg0);
+    if (done) {
+        *o |= nan;
+        return;
+    }
     const int np = any ? g1 - g0 + 1 : 0;                // private pieces
     // prefix pieces of this row
     int pn = 0, pu = 0, pr = 0;
@@ -531,7 +591,6 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
         slot_of(i, part, ml, st, r);
         top = fmaxf(top, ml[2 * r]);
     }
-    const int cg0 = blockIdx.y * 16 + 2 * int(threadIdx.x >> 5);
     f32x4 sum[2] = {zero4(), zero4()};
     for (int i = 0; i < np + pn; ++i) {
         slot_of(i, part, ml, st, r);
@@ -549,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
         const f32x2 v = {sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv};
         out[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
     }
-    *reinterpret_cast<u32x4*>(A.o + row * kMlaLatent + 4 * cg0) = out;
+    *o = out | nan;
     if (A.lse && blockIdx.y == 0 && threadIdx.x < 32)
         A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
 }

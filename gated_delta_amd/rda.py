@@ -171,6 +171,9 @@ def _stream_handle(stream) -> ctypes.c_void_p:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device):
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == tuple(shape) \
+            and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -423,6 +426,30 @@ def _need_gpu(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+class _On:
+    """The device of a call's tensors made current for its launch: kernels go
+    to the current device, whatever the stream's."""
+
+    def __init__(self, dev: torch.device):
+        self.index = dev.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _stream_on(dev: torch.device, stream) -> ctypes.c_void_p:
+    """The given stream, or the current one of the tensors' device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
 def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """A tensor whose rows (all but the first axis) are contiguous; returns
     the distance between rows in elements."""
@@ -491,10 +518,10 @@ def rda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale
         lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (Tq, H), dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         st = lib_.rda_mla_prefill(_ptr(q), qs, _ptr(kv), ks, _ptr(k_pe), ps, _ptr(cq), _ptr(ck),
                                   1 if cq is None else cq.numel() - 1, Tq, Tk, H, float(scale),
-                                  int(bool(causal)), _ptr(o), _ptr(lse), _stream_handle(stream))
+                                  int(bool(causal)), _ptr(o), _ptr(lse), _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_mla_prefill")
     return o, lse
@@ -556,13 +583,13 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
     if workspace is None:
         workspace = _workspace(lib_.rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)),
                                dev, stream)
-    with torch.cuda.device(dev):
+    with _On(dev):
         st = lib_.rda_mla_decode(_ptr(q), _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
                                  _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
                                  _ptr(prefix_table) if prefix_len > 0 else None, prefix_len, B, T,
                                  H, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(),
-                                 _stream_handle(stream))
+                                 _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_mla_decode")
     return o, lse
@@ -605,11 +632,11 @@ def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
         raise ValueError("cu_seqlens must have one entry more than block_table has rows")
     if weight is not None:
         _need(weight, "weight", torch.float32, (RDA_MLA_LATENT,), dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         st = lib_.rda_mla_append(_ptr(kv), stride, _ptr(weight), float(eps), _ptr(cu), N, T,
                                  _ptr(kv_lens), _ptr(block_table), block_table.shape[1],
                                  _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
-                                 _stream_handle(stream))
+                                 _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_mla_append")
     return cache
@@ -668,12 +695,12 @@ def rda_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     _need(out_tokens, "out_tokens", torch.int32, (B, T), dev)
     if workspace is None:
         workspace = _workspace(lib_.rda_verify_drafts_workspace_bytes(B, V), dev, stream)
-    with torch.cuda.device(dev):
+    with _On(dev):
         st = lib_.rda_verify_drafts(_ptr(target), ts, _ptr(draft) if T > 1 else None, ds,
                                     _ptr(draft_tokens), _ptr(uniforms), _ptr(num_drafts), B, T - 1,
                                     V, _ptr(accept), _ptr(out_tokens), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(),
-                                    _stream_handle(stream))
+                                    _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_verify_drafts")
     return accept, out_tokens
