@@ -282,8 +282,6 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
     const float c = A.scale * kLog2e;
     float m = -INFINITY, mu = 0.f, lsum = 0.f;
     f32x16 acc[8] = {};
-#pragma unroll
-    for (int i = 0; i < 36; ++i) asm volatile("" : "+v"(qf[i]));
 
     const uint32_t group_lds = lds_addr(&lds.tile[kw * kBuf]);
     const int share = kRG == 2 ? w : half;   // this wave's part of a tile
@@ -300,6 +298,10 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
         const int t = t0 + d * kKW + kw;
         if (t < t1) issue(t, d);
     }
+    // the queries have arrived before the loop: no wait of the compiler's own
+    // stands in it
+#pragma unroll
+    for (int i = 0; i < 36; ++i) asm volatile("" : "+v"(qf[i]));
     const int own = (t1 - t0 - kw + kKW - 1) / kKW;   // the other pair may have one more
     for (int i = 0; i < own; ++i) {
         const int t = t0 + i * kKW + kw, buf = i % kBuf;
@@ -319,10 +321,24 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
         const uint32_t base = group_lds + buf * kTileBytes;
         const int k0 = t * kTile;
         const Addr addr{here(addr0.k), here(addr0.pe), here(addr0.v)};
+        // operands are read a batch ahead of their products: with one wave per
+        // SIMD nothing else covers the latency of LDS
+        constexpr int kB = 6;
         f32x16 s = {};
+        bf16x8 ko[2][kB];
 #pragma unroll
-        for (int mm = 0; mm < 36; ++mm)
-            s = mfma32(k_op(addr, base, mm), qf[mm], s);
+        for (int e = 0; e < kB; ++e) ko[0][e] = k_op(addr, base, e);
+#pragma unroll
+        for (int n = 0; n < 36 / kB; ++n) {
+            if (n + 1 < 36 / kB) {
+#pragma unroll
+                for (int e = 0; e < kB; ++e) ko[(n + 1) & 1][e] = k_op(addr, base, kB * (n + 1) + e);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < kB; ++e) s = mfma32(ko[n & 1][e], qf[kB * n + e], s);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         const bool masked = k0 + kTile > all_see;
         if (masked) {
 #pragma unroll
@@ -358,11 +374,27 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
             clean_rows(group_lds + buf * kTileBytes, share * kIssue, kIssue, l);
             raw_barrier();
         }
+        constexpr int kV = 4;   // value operands per batch
+        bf16x8 vo[2][kV];
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+        for (int e = 0; e < kV; ++e) vo[0][e] = v_op(addr, base + 512 * half, e >> 1, e & 1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                acc[b] = mfma32(v_op(addr, base + 512 * half, b, k), p[k], acc[b]);
+        for (int n = 0; n < 16 / kV; ++n) {
+            if (n + 1 < 16 / kV) {
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const int x = kV * (n + 1) + e;
+                    vo[(n + 1) & 1][e] = v_op(addr, base + 512 * half, x >> 1, x & 1);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const int x = kV * n + e;
+                acc[x >> 1] = mfma32(vo[n & 1][e], p[x & 1], acc[x >> 1]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     if (kKW > 1 && own < steps) {
         raw_barrier();
@@ -584,22 +616,42 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
             r = pr;
         }
     };
-    const float *part, *ml;
-    int st, r;
+    // eight pieces' sums at a time, all loads before their use
+    constexpr int kN = 8;
+    const int n = np + pn;
     float top = -INFINITY, total = 0.f;
-    for (int i = 0; i < np + pn; ++i) {
-        slot_of(i, part, ml, st, r);
-        top = fmaxf(top, ml[2 * r]);
-    }
     f32x4 sum[2] = {zero4(), zero4()};
-    for (int i = 0; i < np + pn; ++i) {
-        slot_of(i, part, ml, st, r);
-        const float x = ml[2 * r];
-        const float f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
-        total = fmaf(ml[2 * r + 1], f, total);
+    for (int i0 = 0; i0 < n; i0 += kN) {
+        f32x2 ml[kN];
+        f32x4 x[kN][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            sum[k] += *reinterpret_cast<const f32x4*>(part + (size_t(cg0 + k) * st + r) * 4) * f;
+        for (int e = 0; e < kN; ++e) {
+            const float *part, *pml;
+            int st, r;
+            slot_of(min(i0 + e, n - 1), part, pml, st, r);
+            ml[e] = *reinterpret_cast<const f32x2*>(pml + 2 * r);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                x[e][k] = *reinterpret_cast<const f32x4*>(part + (size_t(cg0 + k) * st + r) * 4);
+        }
+        float most = top;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) most = fmaxf(most, ml[e][0]);
+        const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - most);
+        top = most;
+        total *= f;
+        sum[0] *= f;
+        sum[1] *= f;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const float w = i0 + e >= n || ml[e][0] == -INFINITY
+                ? 0.f : __builtin_amdgcn_exp2f(ml[e][0] - most);
+            if (w != 0.f) {   // (a piece without keys has no sums to speak of)
+                total = fmaf(ml[e][1], w, total);
+                sum[0] += x[e][0] * w;
+                sum[1] += x[e][1] * w;
+            }
+        }
     }
     const float inv = inverse(total);
     u32x4 out;
