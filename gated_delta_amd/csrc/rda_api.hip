@@ -67,14 +67,14 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // The plan of rda_mla_decode (sizes in A) and its workspace: with ws, the
 // pointers too.  Returns the bytes.
 //
-// Query rows go in blocks of 64 (two row groups) where a sequence has more
-// than 32, in blocks of 32 otherwise.  Every workgroup takes an equal share
-// of the tiles, but at least min_tiles: a share that small costs more in
-// partial sums (64 KiB per 32 rows) than in tiles (36 KiB each).
+// Query rows go in blocks of 32, 64 or 128 (1, 2 or 4 row waves), whichever
+// holds a sequence's rows.  Every workgroup takes an equal share of the tiles,
+// but at least min_tiles: a share that small costs more in partial sums (64 KiB
+// per 32 rows) than in tiles (36 KiB each).
 size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
-    A.row_groups = unit_rows > 32 ? 2 : 1;
-    A.row_blocks = int32_t((unit_rows + 32 * A.row_groups - 1) / (32 * A.row_groups));
+    A.row_waves = unit_rows > 64 ? 4 : unit_rows > 32 ? 2 : 1;
+    A.row_blocks = int32_t((unit_rows + 32 * A.row_waves - 1) / (32 * A.row_waves));
     A.min_tiles = 4;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -84,19 +84,21 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     };
     const size_t units = size_t(A.batch) * A.row_blocks;
     A.meta = reinterpret_cast<int32_t*>(take(units * 2 * sizeof(int32_t)));
-    const size_t slots = (units + kMlaWorkgroups) * 32 * A.row_groups;
+    const size_t slots = (units + kMlaWorkgroups) * 32 * A.row_waves;
     A.part = reinterpret_cast<float*>(take(slots * RDA_MLA_LATENT * sizeof(float)));
     A.part_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
-    A.prefix_groups = 1;
+    A.prefix_waves = 1;
     A.prefix_units = 0;
     A.prefix_per = 1;
     if (A.prefix_len > 0 && rows > 0) {
-        A.prefix_groups = rows > 32 ? 2 : 1;
-        A.prefix_units = int32_t((rows + 32 * A.prefix_groups - 1) / (32 * A.prefix_groups));
+        // blocks of 128 rows once they fill the chip with long shares, else
+        // blocks of 32, whose four waves share out the tiles
         const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
+        A.prefix_waves = (rows + 127) / 128 * tiles >= 8 * kMlaWorkgroups ? 4 : 1;
+        A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
         const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
         A.prefix_per = share > 8 ? share : 8;
-        const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_groups;
+        const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_waves;
         A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));
     }

@@ -347,9 +347,9 @@ struct MlaDecodeArgs {
     uint16_t* o;                 // [B, T, H, 512]
     float* lse;                  // [B, T, H] or nullptr
     // plan (mla_decode_plan): a sequence's query rows in row_blocks blocks of
-    // 32 row_groups, all query rows in prefix_units blocks of 32 prefix_groups
-    int32_t row_groups, row_blocks, min_tiles;
-    int32_t prefix_groups, prefix_units;
+    // 32 row_waves, all query rows in prefix_units blocks of 32 prefix_waves
+    int32_t row_waves, row_blocks, min_tiles;
+    int32_t prefix_waves, prefix_units;
     int64_t prefix_per;          // prefix tiles per workgroup
     // workspace
     int32_t* meta;               // per unit: first and last workgroup, or -1

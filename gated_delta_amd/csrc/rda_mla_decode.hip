@@ -10,17 +10,22 @@
 // from memory once for all the query rows of a workgroup: 1152 bytes against
 // 2176 operations per query row.  As in the prefill the products are
 // transposed, S^T = C Q^T and O^T = C^T P^T, a lane owns one query row, and P
-// stays in registers.  Two waves hold the same 32 query rows (576 x 32 bf16
-// of Q, 144 registers) and half of the latent channels each (256 x 32 fp32 of
-// O^T, 128 registers): both form S^T, which saves the exchange.  The 4 waves
-// of a workgroup are kRG such pairs that share tiles of 32 cached rows x
-// 2 / kRG pairs that take tiles in turn and merge their sums at the end.
+// stays in registers.  A wave holds 32 query rows whole: 576 x 32 bf16 of Q
+// (144 registers) and 512 x 32 fp32 of O^T (all 256 accumulation registers).
+// What bounds the products is LDS: an operand of 1 KiB feeds one product of
+// 32 cycles, and the CU's 128 bytes a cycle are just that for its 4 SIMDs; a
+// wave with a part of the channels would read the row operands again.
+// The 4 waves of a workgroup are kRW row waves x 4 / kRW key waves: row waves
+// share a tile of 32 cached rows, key waves take tiles in turn and merge their
+// sums at the end.
 //
 // The work is a list of tiles, unit after unit (a unit: the query rows of one
 // sequence, or a block of all query rows for the prefix), cut into equal
 // pieces, one per workgroup, whatever the sequences' lengths: they are read
 // on the device.  A workgroup that covers a whole unit writes its output; the
 // others write partial sums that the combine kernel joins.
+#include <type_traits>
+
 #include "rda_internal.h"
 #include "rda_mla.h"
 
@@ -55,12 +60,10 @@ struct Lds {
     int unit, first;        // where this workgroup's piece begins
 };
 
-// LDS byte offsets of this lane's operands, from a tile's start: the others
-// differ by exclusive-or of granule bits and by constants.
-struct Addr {
+// LDS byte offsets of this lane's operands, from a tile's start.
+struct Lane {
     int k, pe, v;
-    __device__ __forceinline__ Addr(int k_, int pe_, int v_) : k(k_), pe(pe_), v(v_) {}
-    __device__ __forceinline__ explicit Addr(int l) {
+    __device__ __forceinline__ explicit Lane(int l) {
         const int r = l & 31, g = l >> 5, j = l & 15;
         k = r * kLatBytes + 16 * (g ^ swz(r));
         pe = kTile * kLatBytes + r * kPeBytes + 16 * (g ^ ((r >> 1) & 7));
@@ -70,20 +73,40 @@ struct Addr {
     }
 };
 
-// Row operand of the tile at LDS address `tile`: values 16 m + 8 g ..
-__device__ __forceinline__ bf16x8 k_op(const Addr& a, uint32_t tile, int m) {
-    return lds_read16(m < 32 ? tile + (a.k ^ (32 * (m & 7))) + 256 * (m >> 3)
-                             : tile + (a.pe ^ (32 * (m & 3))));
-}
+// Addresses in one tile: the granule bits that a swizzle turns over are an
+// exclusive-or per lane, all else is a constant in the read instruction (the
+// sums are made opaque, or the compiler adds those constants per read).
+struct RowAddr {
+    uint32_t k[8], pe[4];
+    __device__ __forceinline__ RowAddr(const Lane& a, uint32_t tile) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) k[m] = here(int(tile) + (a.k ^ (32 * m)));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) pe[m] = here(int(tile) + (a.pe ^ (32 * m)));
+    }
+    // values 16 m + 8 g .. of row l % 32
+    __device__ __forceinline__ bf16x8 op(int m) const {
+        return lds_read16(m < 32 ? k[m & 7] + 256 * (m >> 3) : pe[m & 3]);
+    }
+};
 
-// C^T operand: channel block b, rows 16 k + 4g + {0..3, 8..11} (rows eight
-// further on have the other lowest bit in their swizzle).
-__device__ __forceinline__ bf16x8 v_op(const Addr& a, uint32_t tile, int b, int k) {
-    const uint32_t at = 256 * (b >> 2) + k * 16 * kLatBytes;
-    const u32x2 x = lds_read_tr8(tile + (a.v ^ (64 * (b & 3))) + at);
-    const u32x2 y = lds_read_tr8(tile + (a.v ^ (64 * (b & 3) + 16)) + 8 * kLatBytes + at);
-    return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
-}
+struct ValAddr {
+    uint32_t v[4], w[4];
+    __device__ __forceinline__ ValAddr(const Lane& a, uint32_t tile) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            v[b] = here(int(tile) + (a.v ^ (64 * b)));
+            w[b] = here(int(tile) + (a.v ^ (64 * b + 16)));   // rows eight further on
+        }
+    }
+    // channel block b of C^T, rows 16 k + 4g + {0..3, 8..11}
+    __device__ __forceinline__ bf16x8 op(int b, int k) const {
+        const uint32_t at = 256 * (b >> 2) + k * 16 * kLatBytes;
+        const u32x2 x = lds_read_tr8(v[b & 3] + at);
+        const u32x2 y = lds_read_tr8(w[b & 3] + at + 8 * kLatBytes);
+        return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+    }
+};
 
 __device__ __forceinline__ int clamp_len(const MlaDecodeArgs& A, int b) {
     const int64_t most = int64_t(A.table_width) << A.page_shift;
@@ -106,30 +129,48 @@ __device__ __forceinline__ const uint16_t* cached_row(const MlaDecodeArgs& A, co
            int64_t(k & ((1 << A.page_shift) - 1)) * kMlaRow;
 }
 
-// Eight rows [k, k + 8) of a tile (its rows 8 group ..): a transfer of 1 KiB
-// per latent part, one for the eight rows' shared channels.  A page holds
-// whole groups of eight.
-__device__ __forceinline__ void issue8(const MlaDecodeArgs& A, const Source& src, int k, int group,
-                                       int lane_id, uint32_t lds) {
-    const int l = here(lane_id);
-    const char* base = reinterpret_cast<const char*>(
-        k < src.len ? cached_row(A, src.table, k) : A.cache);
-    const uint32_t lat = lds + group * 8 * kLatBytes;
-    const uint32_t pe = lds + kTile * kLatBytes + group * 8 * kPeBytes;
-    const int pr = l >> 3, pj = (l & 7) ^ ((4 * group + (pr >> 1)) & 7);
-    const uint32_t pe_off = pr * kRowBytes + kLatBytes + 16 * pj;
-    const uint32_t lane = 16 * (l ^ (group & 1));
-    if (k + 8 <= src.len) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) dma16_at(base + r * kRowBytes, lane ^ (32 * r), lat + r * kLatBytes);
-        dma16_at(base, pe_off, pe);
-    } else {   // rows behind the last one are zeros
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            dma16_at(k + r < src.len ? base + r * kRowBytes : reinterpret_cast<const char*>(kZeros),
-                     lane ^ (32 * r), lat + r * kLatBytes);
-        dma16_from(k + pr < src.len ? base + pe_off : reinterpret_cast<const char*>(kZeros), pe);
+// The transfers of eight rows [k, k + 8) of a tile (its rows 8 group ..): one of
+// 1 KiB per latent part, one for the eight rows' shared channels.  A page holds
+// whole groups of eight.  Rows from `end` on are read as zeros.
+struct Fetch {
+    const char* base;     // row k
+    int valid;            // rows before `end`
+    uint32_t lds, odd;    // the tile, the group's lowest bit
+    int group;
+
+    __device__ __forceinline__ Fetch(const MlaDecodeArgs& A, int page, int k, int end, int group_,
+                                     uint32_t tile) {
+        group = group_;
+        valid = end - k;
+        lds = tile;
+        base = reinterpret_cast<const char*>(
+            A.cache + int64_t(page) * A.page_stride +
+            int64_t(k & ((1 << A.page_shift) - 1)) * kMlaRow);
     }
+    // transfer i of 0..8
+    __device__ __forceinline__ void issue(int i, int lane_id) const {
+        const char* const zeros = reinterpret_cast<const char*>(kZeros);
+        const int l = here(lane_id);
+        if (i < 8) {
+            dma16_at(i < valid ? base + i * kRowBytes : zeros, (16 * (l ^ (group & 1))) ^ (32 * i),
+                     lds + (group * 8 + i) * kLatBytes);
+        } else {
+            const int r = l >> 3, j = (l & 7) ^ ((4 * group + (r >> 1)) & 7);
+            const uint64_t at = uint64_t(base) + uint32_t(r * kRowBytes + kLatBytes + 16 * j);
+            const uint64_t z = uint64_t(zeros);
+            const bool ok = r < valid;   // (halves apart: a select, not a branch)
+            const uint64_t from = uint64_t(ok ? uint32_t(at >> 32) : uint32_t(z >> 32)) << 32 |
+                                  (ok ? uint32_t(at) : uint32_t(z));
+            dma16_from(reinterpret_cast<const void*>(from),
+                       lds + kTile * kLatBytes + group * 8 * kPeBytes);
+        }
+    }
+};
+
+// The page of row k (any page where k lies behind the table's rows).
+__device__ __forceinline__ int page_of(const MlaDecodeArgs& A, const Source& src, int k) {
+    const int at = k < src.len ? k >> A.page_shift : 0;
+    return src.len > 0 ? min(max(((const_i32*)src.table)[at], 0), A.num_pages - 1) : 0;
 }
 
 // Infinities and NaN in the latent parts of `n` groups of eight rows to zero.
@@ -149,7 +190,7 @@ struct Sink {
     int rows;          // query rows of the unit
     float* part;       // [kGroups][unit rows][4]
     float* ml;         // [unit rows][2]
-    int stride;        // unit rows (32 kRG)
+    int stride;        // unit rows (32 kRW)
 };
 
 __device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x,
@@ -177,100 +218,152 @@ __device__ __forceinline__ void put_ml(const MlaDecodeArgs& A, const Sink& S, in
 
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// x * a with x kept in an accumulation register on every path: written plainly
-// the compiler holds the sums in ordinary registers between the tiles and
-// moves all of them twice per tile.  (x's last product is a tile ago, so no
-// wait for the matrix core stands here.)
-__device__ __forceinline__ float scale_acc(float x, float a) {
-    float t;
-    asm("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %2, %1\n\tv_accvgpr_write_b32 %0, %1"
-        : "+a"(x), "=&v"(t)
-        : "v"(a));
-    return x;
+// O^T of a wave: 16 blocks of 32 channels, block b in the accumulation
+// registers a[16 b] .. a[16 b + 15], written and read by the statements below
+// only.  The compiler is not told that they hold values (left to it, a sum that
+// fills that whole file is copied to memory and back around every branch), but
+// that every statement may change them, so it keeps nothing of its own there;
+// the scores' products, which it would place there too, have ordinary
+// registers.  It does not see matrix products in here either: each waits the
+// two states that ordinary arithmetic needs before one reads its result
+// (s_nop 1), and settle / scores_done stand before a result is read.
+#define RDA_A10(t) "a" #t "0", "a" #t "1", "a" #t "2", "a" #t "3", "a" #t "4", "a" #t "5", \
+                   "a" #t "6", "a" #t "7", "a" #t "8", "a" #t "9"
+#define RDA_ALL_ACC RDA_A10(), RDA_A10(1), RDA_A10(2), RDA_A10(3), RDA_A10(4), RDA_A10(5),    \
+    RDA_A10(6), RDA_A10(7), RDA_A10(8), RDA_A10(9), RDA_A10(10), RDA_A10(11), RDA_A10(12),    \
+    RDA_A10(13), RDA_A10(14), RDA_A10(15), RDA_A10(16), RDA_A10(17), RDA_A10(18), RDA_A10(19),\
+    RDA_A10(20), RDA_A10(21), RDA_A10(22), RDA_A10(23), RDA_A10(24), "a250", "a251", "a252",  \
+    "a253", "a254", "a255"
+
+template <int kN, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+    if constexpr (kN > 0) {
+        unrolled<kN - 1>(f);
+        f(std::integral_constant<int, kN - 1>{});
+    }
 }
 
-// A sum out of its accumulation register (see scale_acc); settle() first.
-__device__ __forceinline__ float read_acc(float x) {
+template <int kReg>
+__device__ __forceinline__ void acc_clear() {
+    asm volatile("v_accvgpr_write_b32 a[%0], 0" ::"n"(kReg) : RDA_ALL_ACC);
+}
+template <int kReg>
+__device__ __forceinline__ void acc_scale(float f) {
+    float t;
+    asm volatile("v_accvgpr_read_b32 %0, a[%2]\n\tv_mul_f32 %0, %1, %0\n\tv_accvgpr_write_b32 a[%2], %0"
+                 : "=&v"(t) : "v"(f), "n"(kReg) : RDA_ALL_ACC);
+}
+template <int kReg>
+__device__ __forceinline__ float acc_read() {
     float y;
-    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(y) : "a"(x));
+    asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(y) : "n"(kReg) : RDA_ALL_ACC);
     return y;
 }
-
-__device__ __forceinline__ f32x4 read_acc4(const f32x16& x, int r) {
-    return f32x4{read_acc(x[r]), read_acc(x[r + 1]), read_acc(x[r + 2]), read_acc(x[r + 3])};
+template <int kBlock>
+__device__ __forceinline__ void acc_product(bf16x8 a, bf16x8 b) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
+                 ::"v"(a), "v"(b), "n"(16 * kBlock), "n"(16 * kBlock + 15) : RDA_ALL_ACC);
 }
-
-// Longer than the last matrix products take to write their registers.
+// Longer than the last products take to write their registers.
 __device__ __forceinline__ void settle() {
-    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15");
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: RDA_ALL_ACC);
 }
 
-// A piece's sums to where they go; with two pairs, joined first.
-template <int kRG>
+// A chain of products for the scores.
+__device__ __forceinline__ void scores_first(f32x16& d, bf16x8 a, bf16x8 b) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0"
+                 : "=&v"(d) : "v"(a), "v"(b) : RDA_ALL_ACC);
+}
+__device__ __forceinline__ void scores_next(f32x16& d, bf16x8 a, bf16x8 b) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+                 : "+v"(d) : "v"(a), "v"(b) : RDA_ALL_ACC);
+}
+__device__ __forceinline__ void scores_done(f32x16& d) {
+    asm volatile("s_nop 15\n\ts_nop 7" : "+v"(d)::RDA_ALL_ACC);
+}
+
+// Registers 4 n .. 4 n + 3.
+template <int kN>
+__device__ __forceinline__ f32x4 acc_read4() {
+    return f32x4{acc_read<4 * kN>(), acc_read<4 * kN + 1>(), acc_read<4 * kN + 2>(), acc_read<4 * kN + 3>()};
+}
+
+// A piece's sums to where they go; with several key waves, joined first.
+template <int kRW>
 __device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const Sink& sink,
-                                       const f32x16 (&acc)[8], float mu, float lsum) {
-    constexpr int kKW = 2 / kRG;
+                                       float mu, float lsum) {
+    constexpr int kKW = 4 / kRW;
     const int w = wave_id(), l = here(threadIdx.x & 63), g = l >> 5;
-    const int half = w & 1, rg = kRG == 2 ? w >> 1 : 0, kw = kRG == 2 ? 0 : w >> 1;
-    const int row = 32 * rg + (l & 31);
+    const int rw = w % kRW, kw = w / kRW;
+    const int row = 32 * rw + (l & 31);
     settle();
     if constexpr (kKW == 1) {
         const float inv = inverse(lsum);
-        if (g == 0 && half == 0) put_ml(A, sink, row, mu, lsum);
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                put4(A, sink, row, 256 * half + 32 * b + d_row(r, g),
-                     read_acc4(acc[b], r), inv);
+        if (32 * rw < sink.rows) {
+            if (g == 0) put_ml(A, sink, row, mu, lsum);
+            unrolled<64>([&](auto q) {
+                constexpr int n = decltype(q)::value;   // block n / 4, registers 4 (n % 4) ..
+                put4(A, sink, row, 32 * (n / 4) + d_row(4 * (n % 4), g), acc_read4<n>(), inv);
+            });
+        }
     } else {
-        // the two pairs' sums meet in LDS; each wave joins half of its channels
-        raw_barrier();   // the tiles are read
+        // 8 of the 16 channel blocks at a time through LDS; each key wave joins
+        // and writes an equal part of them
         if (g == 0) {
             lds.ml[w][0][l] = mu;
             lds.ml[w][1][l] = lsum;
         }
-        f32x4* mine = reinterpret_cast<f32x4*>(&lds.tile[w]);
+        constexpr int kPart = 8 / kKW;
+        float f[kKW], total = 0.f, top = -INFINITY;
+        unrolled<2>([&](auto ph) {
+            constexpr int phase = decltype(ph)::value;
+            raw_barrier();   // the tiles, or the phase before, are read
+            f32x4* mine = reinterpret_cast<f32x4*>(&lds.tile[w]);
+            unrolled<32>([&](auto q) {
+                constexpr int n = decltype(q)::value;
+                mine[n * 64 + l] = acc_read4<32 * phase + n>();
+            });
+            raw_barrier();
+            if (phase == 0) {
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+                for (int k = 0; k < kKW; ++k) top = fmaxf(top, lds.ml[k * kRW + rw][0][l & 31]);
 #pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                mine[(b * 4 + r / 4) * 64 + l] = read_acc4(acc[b], r);
-        raw_barrier();
-        float f[2], total = 0.f, top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) top = fmaxf(top, lds.ml[2 * k + half][0][l & 31]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float x = lds.ml[2 * k + half][0][l & 31];
-            f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
-            total = fmaf(lds.ml[2 * k + half][1][l & 31], f[k], total);
-        }
-        if (w == 0 && g == 0) put_ml(A, sink, row, top, total);
-        const float inv = inverse(total);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int blk = 4 * kw + b;
-                const f32x4 x = reinterpret_cast<const f32x4*>(&lds.tile[half])[(blk * 4 + r) * 64 + l];
-                const f32x4 y = reinterpret_cast<const f32x4*>(&lds.tile[2 + half])[(blk * 4 + r) * 64 + l];
-                put4(A, sink, row, 256 * half + 32 * blk + d_row(4 * r, g), x * f[0] + y * f[1], inv);
+                for (int k = 0; k < kKW; ++k) {
+                    const float x = lds.ml[k * kRW + rw][0][l & 31];
+                    f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
+                    total = fmaf(lds.ml[k * kRW + rw][1][l & 31], f[k], total);
+                }
+                if (kw == 0 && g == 0) put_ml(A, sink, row, top, total);
             }
+            const float inv = inverse(total);
+#pragma unroll
+            for (int b = 0; b < kPart; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int blk = kPart * kw + b;
+                    f32x4 sum = zero4();
+#pragma unroll
+                    for (int k = 0; k < kKW; ++k)
+                        sum += reinterpret_cast<const f32x4*>(
+                                   &lds.tile[k * kRW + rw])[(blk * 4 + r) * 64 + l] * f[k];
+                    put4(A, sink, row, 32 * (8 * phase + blk) + d_row(4 * r, g), sum, inv);
+                }
+        });
     }
     raw_barrier();   // the next piece refills the tiles
 }
 
-// One piece: tiles [t0, t1) of a source for 32 kRG query rows.
-template <int kRG, bool kCausal>
-__device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Addr& addr0,
+// One piece: tiles [t0, t1) of a source for 32 kRW query rows.
+template <int kRW, bool kCausal>
+__device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Lane& lane,
                                       const Source& src, int t0, int t1, const Sink& sink) {
-    constexpr int kKW = 2 / kRG;        // pairs that take tiles in turn
-    constexpr int kBuf = 2 * kRG;       // tile buffers of such a pair (or of both)
-    constexpr int kIssue = 2 / kRG;     // groups of eight rows that a wave fetches
+    constexpr int kKW = 4 / kRW;        // key waves
+    constexpr int kBuf = kRW;           // tile buffers of a key wave's group
+    constexpr int kIssue = 4 / kRW;     // groups of eight rows that a wave fetches
+    constexpr int kDma = 9 * kIssue;    // transfers of a wave per tile
     const int w = wave_id(), l = threadIdx.x & 63, g = l >> 5;
-    const int half = w & 1, rg = kRG == 2 ? w >> 1 : 0, kw = kRG == 2 ? 0 : w >> 1;
-    const int row = 32 * rg + (l & 31);
+    const int rw = w % kRW, kw = w / kRW;
+    const int row = 32 * rw + (l & 31);
     const int rrow = min(row, sink.rows - 1);
     const uint16_t* qrow = A.q + (sink.row0 + rrow) * kMlaRow;
     bf16x8 qf[36];
@@ -281,132 +374,159 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const Ad
     const int all_see = kCausal ? src.len - (A.tokens - 1) : src.len;
     const float c = A.scale * kLog2e;
     float m = -INFINITY, mu = 0.f, lsum = 0.f;
-    f32x16 acc[8] = {};
+    unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
 
     const uint32_t group_lds = lds_addr(&lds.tile[kw * kBuf]);
-    const int share = kRG == 2 ? w : half;   // this wave's part of a tile
-    auto issue = [&](int t, int buf) {
+    const int end = min(src.len, t1 * kTile);
+    // this wave's part of tile t, given its pages
+    auto first_row = [&](int t, int n) { return t * kTile + 8 * (rw * kIssue + n); };
+    auto issue = [&](int t, int buf, const int (&page)[kIssue]) {
 #pragma unroll
-        for (int i = 0; i < kIssue; ++i) {
-            const int group = share * kIssue + i;
-            issue8(A, src, t * kTile + 8 * group, group, l, group_lds + buf * kTileBytes);
+        for (int n = 0; n < kIssue; ++n) {
+            const Fetch f(A, page[n], first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
+#pragma unroll
+            for (int x = 0; x < 9; ++x) f.issue(x, l);
         }
     };
-    const int steps = (t1 - t0 + kKW - 1) / kKW;
+    auto pages = [&](int t, int (&page)[kIssue]) {
 #pragma unroll
-    for (int d = 0; d < kBuf - 1; ++d) {
-        const int t = t0 + d * kKW + kw;
-        if (t < t1) issue(t, d);
+        for (int n = 0; n < kIssue; ++n) page[n] = page_of(A, src, first_row(t, n));
+    };
+    // (a tile behind the last one is fetched too, as zeros: the number of
+    // transfers in flight is the same in every step)
+    int page[kIssue];
+    constexpr int kLead = kBuf > 1 ? kBuf - 1 : 1;   // tiles fetched ahead of the loop
+#pragma unroll
+    for (int d = 0; d < kLead; ++d) {
+        pages(t0 + d * kKW + kw, page);
+        issue(t0 + d * kKW + kw, d, page);
     }
+    pages(t0 + kLead * kKW + kw, page);
     // the queries have arrived before the loop: no wait of the compiler's own
     // stands in it
 #pragma unroll
     for (int i = 0; i < 36; ++i) asm volatile("" : "+v"(qf[i]));
-    const int own = (t1 - t0 - kw + kKW - 1) / kKW;   // the other pair may have one more
+    const int steps = (t1 - t0 + kKW - 1) / kKW;
+    const int own = (t1 - t0 - kw + kKW - 1) / kKW;   // others may have one more
+    const bool idle = 32 * rw >= sink.rows;           // a row wave without rows
     for (int i = 0; i < own; ++i) {
         const int t = t0 + i * kKW + kw, buf = i % kBuf;
         // this wave's part of tile i has landed once only later tiles' parts
         // are on their way
-        if (kBuf == 4 && t + 2 * kKW < t1) wait_vm<2 * 9 * kIssue>();
-        else if (kBuf == 4 && t + kKW < t1) wait_vm<9 * kIssue>();
-        else wait_vm<0>();
-        raw_barrier();   // everyone's part has, and tile i - 1 is read
-        const int next = t + (kBuf - 1) * kKW;
-        if (next < t1) issue(next, (i + kBuf - 1) % kBuf);
+        if constexpr (kBuf > 1) {
+            wait_vm<(kBuf - 2) * kDma>();
+            raw_barrier();   // everyone's part has, and tile i - 1 is read
+            issue(t + kLead * kKW, (i + kLead) % kBuf, page);
+            pages(t + (kLead + 1) * kKW, page);
+        } else {
+            wait_vm<0>();
+        }
+        const uint32_t base = group_lds + buf * kTileBytes;
+        const int k0 = t * kTile;
         // several new tokens: 0 * inf from a row that only later ones see would
         // reach the earlier ones, so the last tiles' latent values are made
         // finite before they serve as values (the combine kernel sets the
         // outputs of the queries that do see such a row)
+        // (all waves meet for it: a step's condition, not a tile's)
         const bool cleaned = kCausal && A.tokens > 1 && (t0 + (i + 1) * kKW) * kTile > all_see;
-        const uint32_t base = group_lds + buf * kTileBytes;
-        const int k0 = t * kTile;
-        const Addr addr{here(addr0.k), here(addr0.pe), here(addr0.v)};
-        // operands are read a batch ahead of their products: with one wave per
-        // SIMD nothing else covers the latency of LDS
-        constexpr int kB = 6;
-        f32x16 s = {};
-        bf16x8 ko[2][kB];
+        bf16x8 p[2];
+        if (!idle) {
+            const RowAddr rows(lane, base);
+            constexpr int kB = 4;   // operands read ahead of their products
+            f32x16 s;
+            bf16x8 ko[2][kB];
 #pragma unroll
-        for (int e = 0; e < kB; ++e) ko[0][e] = k_op(addr, base, e);
+            for (int e = 0; e < kB; ++e) ko[0][e] = rows.op(e);
 #pragma unroll
-        for (int n = 0; n < 36 / kB; ++n) {
-            if (n + 1 < 36 / kB) {
+            for (int n = 0; n < 36 / kB; ++n) {
+                if (n + 1 < 36 / kB) {
 #pragma unroll
-                for (int e = 0; e < kB; ++e) ko[(n + 1) & 1][e] = k_op(addr, base, kB * (n + 1) + e);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int e = 0; e < kB; ++e) s = mfma32(ko[n & 1][e], qf[kB * n + e], s);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        const bool masked = k0 + kTile > all_see;
-        if (masked) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (d_row(r, 0) >= limit - k0 - 4 * g) s[r] = -INFINITY;
-        }
-        float top = s[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-        top = fmaxf(top, other_half(top));
-        // the reference moves only when a row outgrows it by 2^8
-        if (__any((top - m) * c > 8.f || (m == -INFINITY && top > m))) {
-            const float mn = fmaxf(m, top);
-            const float mun = mn == -INFINITY ? 0.f : mn * c;
-            const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
-            m = mn;
-            mu = mun;
-            lsum *= a;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[b][r] = scale_acc(acc[b][r], a);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -mu));
-            lsum += s[r];
-        }
-        const bf16x8 p[2] = {pack8<0>(s), pack8<8>(s)};
-        if (cleaned) {
-            raw_barrier();
-            clean_rows(group_lds + buf * kTileBytes, share * kIssue, kIssue, l);
-            raw_barrier();
-        }
-        constexpr int kV = 4;   // value operands per batch
-        bf16x8 vo[2][kV];
-#pragma unroll
-        for (int e = 0; e < kV; ++e) vo[0][e] = v_op(addr, base + 512 * half, e >> 1, e & 1);
-#pragma unroll
-        for (int n = 0; n < 16 / kV; ++n) {
-            if (n + 1 < 16 / kV) {
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    const int x = kV * (n + 1) + e;
-                    vo[(n + 1) & 1][e] = v_op(addr, base + 512 * half, x >> 1, x & 1);
+                    for (int e = 0; e < kB; ++e) ko[(n + 1) & 1][e] = rows.op(kB * (n + 1) + e);
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                const int x = kV * n + e;
-                acc[x >> 1] = mfma32(vo[n & 1][e], p[x & 1], acc[x >> 1]);
+                for (int e = 0; e < kB; ++e) {
+                    if (n + e == 0) scores_first(s, ko[0][0], qf[0]);
+                    else scores_next(s, ko[n & 1][e], qf[kB * n + e]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            scores_done(s);
+            if (k0 + kTile > all_see) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (d_row(r, 0) >= limit - k0 - 4 * g) s[r] = -INFINITY;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+            top = fmaxf(top, other_half(top));
+            // the reference moves only when a row outgrows it by 2^8
+            if (__any((top - m) * c > 8.f || (m == -INFINITY && top > m))) {
+                const float mn = fmaxf(m, top);
+                const float mun = mn == -INFINITY ? 0.f : mn * c;
+                const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
+                m = mn;
+                mu = mun;
+                lsum *= a;
+                unrolled<256>([a](auto q) { acc_scale<decltype(q)::value>(a); });
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -mu));
+                lsum += s[r];
+            }
+            p[0] = pack8<0>(s);
+            p[1] = pack8<8>(s);
+        }
+        if (cleaned) {
+            if constexpr (kRW > 1) raw_barrier();
+            if (k0 + kTile > all_see) clean_rows(base, rw * kIssue, kIssue, l);
+            if constexpr (kRW > 1) raw_barrier();
+        }
+        if (!idle) {
+            constexpr int kV = 4;   // value operands read ahead
+            const ValAddr vals(lane, base);
+            bf16x8 vo[2][kV];
+#pragma unroll
+            for (int e = 0; e < kV; ++e) vo[0][e] = vals.op(e >> 1, e & 1);
+            unrolled<32 / kV>([&](auto q) {
+                constexpr int n = decltype(q)::value;
+                if constexpr (n + 1 < 32 / kV) {
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) {
+                        const int x = kV * (n + 1) + e;
+                        vo[(n + 1) & 1][e] = vals.op(x >> 1, x & 1);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                unrolled<kV>([&](auto q2) {
+                    constexpr int e = decltype(q2)::value, x = kV * n + e;
+                    acc_product<(x >> 1)>(vo[n & 1][e], p[x & 1]);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+        if constexpr (kBuf == 1) {
+            // the wave's own tile is read: fetch its next one
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue(t + kKW, 0, page);
+            pages(t + 2 * kKW, page);
         }
     }
-    if (kKW > 1 && own < steps) {
-        raw_barrier();
-        if (kCausal && A.tokens > 1 && (t0 + steps * kKW) * kTile > all_see) {
+    wait_vm<0>();   // the tiles behind the last: nothing may land later
+    if constexpr (kRW == 2) {
+        if (own < steps) {   // the other key wave's group meets here
             raw_barrier();
-            raw_barrier();
+            if (kCausal && A.tokens > 1 && (t0 + steps * kKW) * kTile > all_see) {
+                raw_barrier();
+                raw_barrier();
+            }
         }
     }
     lsum += other_half(lsum);
     mu = m == -INFINITY ? -INFINITY : mu;
-
-    finish<kRG>(A, lds, sink, acc, mu, lsum);
+    finish<kRW>(A, lds, sink, mu, lsum);
 }
 
 // A value that every lane holds alike, in scalar registers.
@@ -419,7 +539,7 @@ __device__ __forceinline__ int64_t uniform_i64(int64_t x) {
 // Tiles of a sequence.
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-template <int kRG>
+template <int kRW>
 __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds lds;
     const int l = threadIdx.x & 63, w = wave_id();
@@ -475,7 +595,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     int unit = __builtin_amdgcn_readfirstlane(lds.unit);
     int first = __builtin_amdgcn_readfirstlane(lds.first);
 
-    const Addr addr(l);
+    const Lane lane(l);
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
     int64_t at = begin;
     while (at < end) {
@@ -491,19 +611,19 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
         const int slot = first == 0 ? unit : units + wg;
         Sink sink;
         sink.final = whole && !A.prefix_len;
-        sink.first_row = 32 * kRG * blk;
+        sink.first_row = 32 * kRW * blk;
         sink.row0 = int64_t(b) * unit_rows + sink.first_row;
-        sink.rows = min(32 * kRG, unit_rows - sink.first_row);
-        sink.part = A.part + size_t(slot) * kGroups * 4 * 32 * kRG;
-        sink.ml = A.part_ml + size_t(slot) * 2 * 32 * kRG;
-        sink.stride = 32 * kRG;
+        sink.rows = min(32 * kRW, unit_rows - sink.first_row);
+        sink.part = A.part + size_t(slot) * kGroups * 4 * 32 * kRW;
+        sink.ml = A.part_ml + size_t(slot) * 2 * 32 * kRW;
+        sink.stride = 32 * kRW;
         if (first == 0 && threadIdx.x == 0) {
             // the workgroups that hold this unit's later pieces
             const int64_t stop = at + n;
             A.meta[2 * unit] = sink.final ? -1 : wg;
             A.meta[2 * unit + 1] = int((stop - 1) / per);
         }
-        piece<kRG, true>(A, lds, addr, Source{A.table + int64_t(b) * A.table_width, len}, first,
+        piece<kRW, true>(A, lds, lane, Source{A.table + int64_t(b) * A.table_width, len}, first,
                          last, sink);
         at += last - first;
         first = 0;
@@ -511,12 +631,12 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     }
 }
 
-// The prefix: every block of 32 kRG query rows walks all prefix rows.
-template <int kRG>
+// The prefix: every block of 32 kRW query rows walks all prefix rows.
+template <int kRW>
 __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds lds;
     const int l = threadIdx.x & 63, wg = blockIdx.x;
-    const Addr addr(l);
+    const Lane lane(l);
     const int64_t rows = int64_t(A.batch) * A.tokens * A.heads;
     const int n = tiles_of(A.prefix_len);
     const int64_t total = int64_t(A.prefix_units) * n;
@@ -529,12 +649,12 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
         Sink sink;
         sink.final = false;
         sink.first_row = 0;
-        sink.row0 = int64_t(unit) * 32 * kRG;
-        sink.rows = int(min(int64_t(32 * kRG), rows - sink.row0));
-        sink.part = A.pre_part + size_t(slot) * kGroups * 4 * 32 * kRG;
-        sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRG;
-        sink.stride = 32 * kRG;
-        piece<kRG, false>(A, lds, addr, Source{A.prefix_table, A.prefix_len}, first, last, sink);
+        sink.row0 = int64_t(unit) * 32 * kRW;
+        sink.rows = int(min(int64_t(32 * kRW), rows - sink.row0));
+        sink.part = A.pre_part + size_t(slot) * kGroups * 4 * 32 * kRW;
+        sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRW;
+        sink.stride = 32 * kRW;
+        piece<kRW, false>(A, lds, lane, Source{A.prefix_table, A.prefix_len}, first, last, sink);
         at += last - first;
     }
 }
@@ -546,10 +666,10 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
 // too), and the products left it out.
 __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeArgs A) {
     __shared__ int bad_s;
-    const int unit = blockIdx.x / A.row_groups, sub = blockIdx.x % A.row_groups;
+    const int unit = blockIdx.x / A.row_waves, sub = blockIdx.x % A.row_waves;
     const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
-    const int stride = 32 * A.row_groups;
+    const int stride = 32 * A.row_waves;
     const int lr = 32 * sub + int(threadIdx.x & 31);     // row in the unit's block
     const int urow = stride * blk + lr;                  // row in the sequence
     const int len = clamp_len(A, b);
@@ -594,13 +714,13 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
     int pn = 0, pu = 0, pr = 0;
     int64_t pg0 = 0;
     if (A.prefix_len) {
-        const int n = tiles_of(A.prefix_len), prows = 32 * A.prefix_groups;
+        const int n = tiles_of(A.prefix_len), prows = 32 * A.prefix_waves;
         pu = int(row / prows);
         pr = int(row - int64_t(pu) * prows);
         pg0 = int64_t(pu) * n / A.prefix_per;
         pn = int((int64_t(pu + 1) * n - 1) / A.prefix_per - pg0) + 1;
     }
-    const int pstride = 32 * A.prefix_groups;
+    const int pstride = 32 * A.prefix_waves;
     auto slot_of = [&](int i, const float*& part, const float*& ml, int& st, int& r) {
         if (i < np) {
             const size_t s = i == 0 ? size_t(unit) : size_t(units) + g0 + i;
@@ -665,15 +785,15 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
         A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
 }
 
-template <int kRG>
+template <int kRW>
 void launch_private(const MlaDecodeArgs& A, hipStream_t stream) {
-    mla_decode_kernel<kRG><<<dim3(kMlaWorkgroups), dim3(kThreads), 0, stream>>>(A);
+    mla_decode_kernel<kRW><<<dim3(kMlaWorkgroups), dim3(kThreads), 0, stream>>>(A);
 }
 
-template <int kRG>
+template <int kRW>
 void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
     const int64_t total = int64_t(A.prefix_units) * ((A.prefix_len + kTile - 1) / kTile);
-    mla_prefix_kernel<kRG><<<dim3(unsigned((total + A.prefix_per - 1) / A.prefix_per)),
+    mla_prefix_kernel<kRW><<<dim3(unsigned((total + A.prefix_per - 1) / A.prefix_per)),
                              dim3(kThreads), 0, stream>>>(A);
 }
 
@@ -681,14 +801,15 @@ void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
 
 hipError_t launch_mla_decode(const MlaDecodeArgs& A, hipStream_t stream) {
     if (A.prefix_len) {
-        if (A.prefix_groups == 2) launch_prefix<2>(A, stream);
+        if (A.prefix_waves == 4) launch_prefix<4>(A, stream);
         else launch_prefix<1>(A, stream);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (A.row_groups == 2) launch_private<2>(A, stream);
+    if (A.row_waves == 4) launch_private<4>(A, stream);
+    else if (A.row_waves == 2) launch_private<2>(A, stream);
     else launch_private<1>(A, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    mla_combine_kernel<<<dim3(unsigned(A.batch * A.row_blocks * A.row_groups), 8), dim3(kThreads), 0,
+    mla_combine_kernel<<<dim3(unsigned(A.batch * A.row_blocks * A.row_waves), 8), dim3(kThreads), 0,
                          stream>>>(A);
     return hipGetLastError();
 }
