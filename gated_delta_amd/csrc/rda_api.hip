@@ -54,12 +54,17 @@ rda_status check_pages(int64_t page_stride, int32_t num_pages, int32_t page_toke
     return RDA_OK;
 }
 
+// Query rows and tiles (of 32 cached rows, for 32 query rows or more) are
+// counted in 32 bits.
+bool mla_tiles_ok(int64_t query_rows, int64_t cached_rows) {
+    return ((query_rows + 31) / 32) * ((cached_rows + 31) / 32) <= INT32_MAX - (1 << 20);
+}
+
 rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, int32_t prefix_len) {
     if (batch < 0 || tokens < 0 || tokens > RDA_DECODE_MAX_TOKENS || heads < 1 || prefix_len < 0)
         return RDA_ERR_SHAPE;
-    // 32-bit indexes of query rows and of tiles
-    if (int64_t(tokens) * heads > (1 << 24) ||
-        int64_t(batch) * tokens * heads > (1 << 26) || prefix_len > (1 << 30))
+    if (int64_t(tokens) * heads > (1 << 24) || int64_t(batch) * tokens * heads > (1 << 26) ||
+        prefix_len > (1 << 30) || !mla_tiles_ok(int64_t(batch) * tokens * heads, prefix_len))
         return RDA_ERR_SHAPE;
     return RDA_OK;
 }
@@ -84,6 +89,7 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     };
     const size_t units = size_t(A.batch) * A.row_blocks;
     A.meta = reinterpret_cast<int32_t*>(take(units * 2 * sizeof(int32_t)));
+    A.bad = reinterpret_cast<int32_t*>(take((units + kMlaWorkgroups) * sizeof(int32_t)));
     const size_t slots = (units + kMlaWorkgroups) * 32 * A.row_waves;
     A.part = reinterpret_cast<float*>(take(slots * RDA_MLA_LATENT * sizeof(float)));
     A.part_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
@@ -97,7 +103,9 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
         A.prefix_waves = (rows + 127) / 128 * tiles >= 8 * kMlaWorkgroups ? 4 : 1;
         A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
         const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
-        A.prefix_per = share > 8 ? share : 8;
+        A.prefix_per = int32_t(share > 8 ? share : 8);
+        A.pre_bad = reinterpret_cast<int32_t*>(
+            take((size_t(A.prefix_units) + kMlaWorkgroups) * sizeof(int32_t)));
         const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_waves;
         A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));
@@ -1126,6 +1134,10 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
     if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
         return st;
     if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
+    if (int64_t(table_width) * page_tokens > INT32_MAX ||
+        !mla_tiles_ok((int64_t(tokens) * num_heads + 31) / 32 * 32 * batch,
+                      int64_t(table_width) * page_tokens))
+        return RDA_ERR_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale)) return RDA_ERR_VALUE;
     if (batch == 0 || tokens == 0) return RDA_OK;
     if (!q || !o || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache) ||

@@ -350,9 +350,10 @@ struct MlaDecodeArgs {
     // 32 row_waves, all query rows in prefix_units blocks of 32 prefix_waves
     int32_t row_waves, row_blocks, min_tiles;
     int32_t prefix_waves, prefix_units;
-    int64_t prefix_per;          // prefix tiles per workgroup
+    int32_t prefix_per;          // prefix tiles per workgroup
     // workspace
     int32_t* meta;               // per unit: first and last workgroup, or -1
+    int32_t *bad, *pre_bad;      // per slot of partial sums
     float *part, *part_ml, *pre_part, *pre_ml;
 };
 hipError_t launch_mla_decode(const MlaDecodeArgs& A, hipStream_t stream);

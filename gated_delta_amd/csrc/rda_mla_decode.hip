@@ -37,7 +37,6 @@ constexpr int kTile = 32;                          // cached rows per tile
 constexpr int kRowBytes = kMlaRow * 2;             // 1152
 constexpr int kLatBytes = kMlaLatent * 2, kPeBytes = kMlaPe * 2;
 constexpr int kTileBytes = kTile * kRowBytes;      // 36864
-constexpr int kGroups = kMlaLatent / 4;            // 4-channel groups of an output row
 
 typedef const __attribute__((address_space(4))) int32_t const_i32;
 
@@ -58,6 +57,7 @@ struct Lds {
     float ml[4][2][32];     // (mu, l) of each wave's rows
     int scan[8];
     int unit, first;        // where this workgroup's piece begins
+    int bad;                // the piece's last tiles held infinities or NaN
 };
 
 // LDS byte offsets of this lane's operands, from a tile's start.
@@ -135,7 +135,7 @@ __device__ __forceinline__ const uint16_t* cached_row(const MlaDecodeArgs& A, co
 struct Fetch {
     const char* base;     // row k
     int valid;            // rows before `end`
-    uint32_t lds, odd;    // the tile, the group's lowest bit
+    uint32_t lds;         // the tile
     int group;
 
     __device__ __forceinline__ Fetch(const MlaDecodeArgs& A, int page, int k, int end, int group_,
@@ -173,13 +173,22 @@ __device__ __forceinline__ int page_of(const MlaDecodeArgs& A, const Source& src
     return src.len > 0 ? min(max(((const_i32*)src.table)[at], 0), A.num_pages - 1) : 0;
 }
 
-// Infinities and NaN in the latent parts of `n` groups of eight rows to zero.
-__device__ __forceinline__ void clean_rows(uint32_t tile, int group, int n, int l) {
-    typedef __attribute__((address_space(3))) u32x4 lds_quad;
+// Infinities and NaN in the latent parts of `n` groups of eight rows to zero;
+// whether there were any.
+__device__ __forceinline__ bool clean_rows(uint32_t tile, int group, int n, int l) {
+    uint32_t bad = 0;
     for (int r = 0; r < 8 * n; ++r) {
-        lds_quad* p = (lds_quad*)(lds_char*)uintptr_t(tile + (8 * group + r) * kLatBytes + 16 * l);
-        *p = __builtin_bit_cast(u32x4, finite_only(__builtin_bit_cast(bf16x8, *p)));
+        lds_u32x4* p = (lds_u32x4*)(lds_char*)uintptr_t(tile + (8 * group + r) * kLatBytes + 16 * l);
+        u32x4 x = *p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = nonfinite_bits(x[i]);
+            bad |= b;
+            x[i] &= ~((b >> 15) * 0xffffu);
+        }
+        *p = x;
     }
+    return __any(bad != 0);
 }
 
 // Where a piece's sums go: the outputs, or a slot of partial sums.
@@ -188,21 +197,25 @@ struct Sink {
     int64_t row0;      // first query row of the unit's block (outputs)
     int first_row;     // the same, from the sequence's first query row
     int rows;          // query rows of the unit
-    float* part;       // [kGroups][unit rows][4]
+    float* part;       // [unit rows][512]
     float* ml;         // [unit rows][2]
-    int stride;        // unit rows (32 kRW)
+    int32_t* bad;      // set where the last tiles held infinities or NaN
 };
 
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    const f32x2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Four channels of a row, and a row's statistics.
 __device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x,
                                      float inv) {
     if (S.final) {
-        if (row >= S.rows) return;
-        const f32x2 a = {x[0] * inv, x[1] * inv}, b = {x[2] * inv, x[3] * inv};
-        *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
-            u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2)),
-                  __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2))};
+        if (row < S.rows)
+            *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
+                u32x2{pack2(x[0] * inv, x[1] * inv), pack2(x[2] * inv, x[3] * inv)};
     } else {
-        *reinterpret_cast<f32x4*>(S.part + (size_t(ch >> 2) * S.stride + row) * 4) = x;
+        *reinterpret_cast<f32x4*>(S.part + size_t(row) * kMlaLatent + ch) = x;
     }
 }
 
@@ -211,8 +224,7 @@ __device__ __forceinline__ void put_ml(const MlaDecodeArgs& A, const Sink& S, in
     if (S.final) {
         if (A.lse && row < S.rows) A.lse[S.row0 + row] = l == 0.f ? -INFINITY : fmaf(mu, kLn2, logf(l));
     } else {
-        S.ml[2 * row] = mu;
-        S.ml[2 * row + 1] = l;
+        *reinterpret_cast<f32x2*>(S.ml + 2 * row) = f32x2{mu, l};
     }
 }
 
@@ -253,11 +265,11 @@ __device__ __forceinline__ void acc_scale(float f) {
     asm volatile("v_accvgpr_read_b32 %0, a[%2]\n\tv_mul_f32 %0, %1, %0\n\tv_accvgpr_write_b32 a[%2], %0"
                  : "=&v"(t) : "v"(f), "n"(kReg) : RDA_ALL_ACC);
 }
-template <int kReg>
-__device__ __forceinline__ float acc_read() {
-    float y;
-    asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(y) : "n"(kReg) : RDA_ALL_ACC);
-    return y;
+// Registers 4 n .. 4 n + 3 to LDS byte address `at` + kOffset (the caller waits).
+template <int kN, int kOffset>
+__device__ __forceinline__ void acc_store(uint32_t at) {
+    asm volatile("ds_write_b128 %0, a[%1:%2] offset:%3"
+                 ::"v"(at), "n"(4 * kN), "n"(4 * kN + 3), "n"(kOffset) : "memory", RDA_ALL_ACC);
 }
 template <int kBlock>
 __device__ __forceinline__ void acc_product(bf16x8 a, bf16x8 b) {
@@ -282,74 +294,56 @@ __device__ __forceinline__ void scores_done(f32x16& d) {
     asm volatile("s_nop 15\n\ts_nop 7" : "+v"(d)::RDA_ALL_ACC);
 }
 
-// Registers 4 n .. 4 n + 3.
-template <int kN>
-__device__ __forceinline__ f32x4 acc_read4() {
-    return f32x4{acc_read<4 * kN>(), acc_read<4 * kN + 1>(), acc_read<4 * kN + 2>(), acc_read<4 * kN + 3>()};
-}
-
-// A piece's sums to where they go; with several key waves, joined first.
+// A piece's sums to where they go, by way of LDS (the tiles' memory): 256
+// channels at a time, 32 rows a wave, so that they leave row by row; the key
+// waves' sums are joined there, each key wave taking an equal part of the rows.
 template <int kRW>
 __device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const Sink& sink,
                                        float mu, float lsum) {
-    constexpr int kKW = 4 / kRW;
-    const int w = wave_id(), l = here(threadIdx.x & 63), g = l >> 5;
+    constexpr int kKW = 4 / kRW, kRows = 32 / kKW;
+    constexpr int kStride = 256 * 4 + 16;   // a row's sums in LDS; 16: other banks
+    static_assert(32 * kStride <= kTileBytes, "a wave's rows fit its tile");
+    const int w = wave_id(), l = here(threadIdx.x & 63);
     const int rw = w % kRW, kw = w / kRW;
-    const int row = 32 * rw + (l & 31);
-    settle();
-    if constexpr (kKW == 1) {
-        const float inv = inverse(lsum);
-        if (32 * rw < sink.rows) {
-            if (g == 0) put_ml(A, sink, row, mu, lsum);
-            unrolled<64>([&](auto q) {
-                constexpr int n = decltype(q)::value;   // block n / 4, registers 4 (n % 4) ..
-                put4(A, sink, row, 32 * (n / 4) + d_row(4 * (n % 4), g), acc_read4<n>(), inv);
-            });
-        }
-    } else {
-        // 8 of the 16 channel blocks at a time through LDS; each key wave joins
-        // and writes an equal part of them
-        if (g == 0) {
-            lds.ml[w][0][l] = mu;
-            lds.ml[w][1][l] = lsum;
-        }
-        constexpr int kPart = 8 / kKW;
-        float f[kKW], total = 0.f, top = -INFINITY;
-        unrolled<2>([&](auto ph) {
-            constexpr int phase = decltype(ph)::value;
-            raw_barrier();   // the tiles, or the phase before, are read
-            f32x4* mine = reinterpret_cast<f32x4*>(&lds.tile[w]);
-            unrolled<32>([&](auto q) {
-                constexpr int n = decltype(q)::value;
-                mine[n * 64 + l] = acc_read4<32 * phase + n>();
-            });
-            raw_barrier();
-            if (phase == 0) {
-#pragma unroll
-                for (int k = 0; k < kKW; ++k) top = fmaxf(top, lds.ml[k * kRW + rw][0][l & 31]);
-#pragma unroll
-                for (int k = 0; k < kKW; ++k) {
-                    const float x = lds.ml[k * kRW + rw][0][l & 31];
-                    f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
-                    total = fmaf(lds.ml[k * kRW + rw][1][l & 31], f[k], total);
-                }
-                if (kw == 0 && g == 0) put_ml(A, sink, row, top, total);
-            }
-            const float inv = inverse(total);
-#pragma unroll
-            for (int b = 0; b < kPart; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int blk = kPart * kw + b;
-                    f32x4 sum = zero4();
-#pragma unroll
-                    for (int k = 0; k < kKW; ++k)
-                        sum += reinterpret_cast<const f32x4*>(
-                                   &lds.tile[k * kRW + rw])[(blk * 4 + r) * 64 + l] * f[k];
-                    put4(A, sink, row, 32 * (8 * phase + blk) + d_row(4 * r, g), sum, inv);
-                }
-        });
+    if (l < 32) {
+        lds.ml[w][0][l] = mu;
+        lds.ml[w][1][l] = lsum;
     }
+    settle();
+    raw_barrier();   // the tiles are read
+    if (threadIdx.x == 0) {
+        *sink.bad = lds.bad;
+        lds.bad = 0;
+    }
+    const uint32_t mine = lds_addr(&lds.tile[w]) + (l & 31) * kStride + 16 * (l >> 5);
+    unrolled<2>([&](auto ph) {
+        constexpr int phase = decltype(ph)::value;
+        if constexpr (phase > 0) raw_barrier();   // the channels before are read
+        unrolled<32>([&](auto q) {
+            constexpr int n = decltype(q)::value;   // block n / 4, channels 8 (n % 4) + 4g ..
+            acc_store<32 * phase + n, 128 * (n / 4) + 32 * (n % 4)>(mine);
+        });
+        raw_barrier();
+#pragma unroll 4
+        for (int i = 0; i < kRows; ++i) {
+            const int r = kw * kRows + i;
+            float top = lds.ml[rw][0][r];
+#pragma unroll
+            for (int k = 1; k < kKW; ++k) top = fmaxf(top, lds.ml[k * kRW + rw][0][r]);
+            float total = 0.f;
+            f32x4 sum = zero4();
+#pragma unroll
+            for (int k = 0; k < kKW; ++k) {
+                const float x = lds.ml[k * kRW + rw][0][r];
+                const float f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
+                total = fmaf(lds.ml[k * kRW + rw][1][r], f, total);
+                sum += *reinterpret_cast<const f32x4*>(
+                           reinterpret_cast<const char*>(&lds.tile[k * kRW + rw]) + r * kStride + 16 * l) * f;
+            }
+            put4(A, sink, 32 * rw + r, 256 * phase + 4 * l, sum, inverse(total));
+            if (phase == 0 && l == 0) put_ml(A, sink, 32 * rw + r, top, total);
+        }
+    });
     raw_barrier();   // the next piece refills the tiles
 }
 
@@ -366,42 +360,34 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
     const int row = 32 * rw + (l & 31);
     const int rrow = min(row, sink.rows - 1);
     const uint16_t* qrow = A.q + (sink.row0 + rrow) * kMlaRow;
-    bf16x8 qf[36];
-#pragma unroll
-    for (int m = 0; m < 36; ++m)
-        qf[m] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qrow + 16 * m + 8 * g));
     const int limit = kCausal ? src.len - (A.tokens - 1 - (sink.first_row + rrow) / A.heads) : src.len;
     const int all_see = kCausal ? src.len - (A.tokens - 1) : src.len;
     const float c = A.scale * kLog2e;
     float m = -INFINITY, mu = 0.f, lsum = 0.f;
-    unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
-
     const uint32_t group_lds = lds_addr(&lds.tile[kw * kBuf]);
     const int end = min(src.len, t1 * kTile);
-    // this wave's part of tile t, given its pages
+    // this wave's part of tile t.  (A tile behind the last one is fetched too, as
+    // zeros: the number of transfers in flight is the same in every step.)
     auto first_row = [&](int t, int n) { return t * kTile + 8 * (rw * kIssue + n); };
-    auto issue = [&](int t, int buf, const int (&page)[kIssue]) {
-#pragma unroll
+    int page = page_of(A, src, first_row(t0 + kw, 0));
+    auto issue = [&](int t, int buf) {
+#pragma unroll 1
         for (int n = 0; n < kIssue; ++n) {
-            const Fetch f(A, page[n], first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
+            const Fetch f(A, page, first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
+            // the page of the fetch after this one
+            page = page_of(A, src, n + 1 < kIssue ? first_row(t, n + 1) : first_row(t + kKW, 0));
 #pragma unroll
             for (int x = 0; x < 9; ++x) f.issue(x, l);
         }
     };
-    auto pages = [&](int t, int (&page)[kIssue]) {
-#pragma unroll
-        for (int n = 0; n < kIssue; ++n) page[n] = page_of(A, src, first_row(t, n));
-    };
-    // (a tile behind the last one is fetched too, as zeros: the number of
-    // transfers in flight is the same in every step)
-    int page[kIssue];
     constexpr int kLead = kBuf > 1 ? kBuf - 1 : 1;   // tiles fetched ahead of the loop
+#pragma unroll 1
+    for (int d = 0; d < kLead; ++d) issue(t0 + d * kKW + kw, d);
+    bf16x8 qf[36];
 #pragma unroll
-    for (int d = 0; d < kLead; ++d) {
-        pages(t0 + d * kKW + kw, page);
-        issue(t0 + d * kKW + kw, d, page);
-    }
-    pages(t0 + kLead * kKW + kw, page);
+    for (int m = 0; m < 36; ++m)
+        qf[m] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qrow + 16 * m + 8 * g));
+    unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
     // the queries have arrived before the loop: no wait of the compiler's own
     // stands in it
 #pragma unroll
@@ -416,8 +402,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
         if constexpr (kBuf > 1) {
             wait_vm<(kBuf - 2) * kDma>();
             raw_barrier();   // everyone's part has, and tile i - 1 is read
-            issue(t + kLead * kKW, (i + kLead) % kBuf, page);
-            pages(t + (kLead + 1) * kKW, page);
+            issue(t + kLead * kKW, (i + kLead) % kBuf);
         } else {
             wait_vm<0>();
         }
@@ -466,10 +451,11 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
                 const float mn = fmaxf(m, top);
                 const float mun = mn == -INFINITY ? 0.f : mn * c;
                 const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
+                const bool first = __all(m == -INFINITY);   // the sums are zeros
                 m = mn;
                 mu = mun;
                 lsum *= a;
-                unrolled<256>([a](auto q) { acc_scale<decltype(q)::value>(a); });
+                if (!first) unrolled<256>([a](auto q) { acc_scale<decltype(q)::value>(a); });
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -481,7 +467,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
         }
         if (cleaned) {
             if constexpr (kRW > 1) raw_barrier();
-            if (k0 + kTile > all_see) clean_rows(base, rw * kIssue, kIssue, l);
+            if (k0 + kTile > all_see && clean_rows(base, rw * kIssue, kIssue, l)) lds.bad = 1;
             if constexpr (kRW > 1) raw_barrier();
         }
         if (!idle) {
@@ -510,8 +496,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
         if constexpr (kBuf == 1) {
             // the wave's own tile is read: fetch its next one
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            issue(t + kKW, 0, page);
-            pages(t + 2 * kKW, page);
+            issue(t + kKW, 0);
         }
     }
     wait_vm<0>();   // the tiles behind the last: nothing may land later
@@ -529,24 +514,16 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
     finish<kRW>(A, lds, sink, mu, lsum);
 }
 
-// A value that every lane holds alike, in scalar registers.
-__device__ __forceinline__ int64_t uniform_i64(int64_t x) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(int(uint32_t(x)));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(int(uint32_t(uint64_t(x) >> 32)));
-    return int64_t(uint64_t(hi) << 32 | lo);
-}
-
 // Tiles of a sequence.
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 template <int kRW>
 __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds lds;
-    const int l = threadIdx.x & 63, w = wave_id();
-    const int G = gridDim.x, wg = blockIdx.x;
+    const int l = threadIdx.x & 63, w = wave_id(), wg = blockIdx.x;
 
     // the number of tiles, and where this workgroup's share begins
-    auto block_sum = [&](int x, int& before) {   // inclusive scan over the workgroup
+    auto block_sum = [&](int x, int& before) {   // x over the workgroup
         int s = x;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -563,33 +540,36 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
             if (k < w) before += lds.scan[k];
             total += lds.scan[k];
         }
-        return total;
+        return __builtin_amdgcn_readfirstlane(total);
     };
-    int64_t total = 0;
-    for (int b0 = 0; b0 < A.batch; b0 += kThreads) {
-        const int b = b0 + int(threadIdx.x);
+    auto tiles_at = [&](int b) { return b < A.batch ? tiles_of(clamp_len(A, b)) : 0; };
+    if (threadIdx.x == 0) lds.bad = 0;
+    const int n0 = tiles_at(threadIdx.x);
+    int before0;
+    const int total0 = block_sum(n0, before0);
+    int total = total0;
+    for (int b0 = kThreads; b0 < A.batch; b0 += kThreads) {
         int before;
-        total += block_sum(b < A.batch ? tiles_of(clamp_len(A, b)) : 0, before);
+        total += block_sum(tiles_at(b0 + int(threadIdx.x)), before);
     }
-    total = uniform_i64(total) * A.row_blocks;
-    const int64_t share = (total + G - 1) / G;
-    const int64_t per = share > A.min_tiles ? share : A.min_tiles;
-    const int64_t begin = per * wg, end = begin + per < total ? begin + per : total;
-    if (begin >= end) return;
-    if (threadIdx.x == 0) lds.unit = -1;
-    int64_t seen = 0;
-    for (int b0 = 0; b0 < A.batch; b0 += kThreads) {
+    total *= A.row_blocks;
+    const int share = (total + kMlaWorkgroups - 1) / kMlaWorkgroups;
+    const int per = share > A.min_tiles ? share : A.min_tiles;
+    if (int64_t(per) * wg >= total) return;
+    const int begin = per * wg, end = min(begin + per, total);
+    for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
         const int b = b0 + int(threadIdx.x);
-        const int n = b < A.batch ? tiles_of(clamp_len(A, b)) : 0;
-        int before;
-        const int sum = block_sum(n, before);
-        const int64_t at = begin - (seen + before) * A.row_blocks;
-        if (n > 0 && at >= 0 && at < int64_t(n) * A.row_blocks) {
-            lds.unit = b * A.row_blocks + int(at / n);
-            lds.first = int(at % n);
+        int n = n0, before = before0, sum = total0;
+        if (b0 > 0) {
+            n = tiles_at(b);
+            sum = block_sum(n, before);
+        }
+        const int at = begin - (seen + before) * A.row_blocks;
+        if (n > 0 && at >= 0 && at < n * A.row_blocks) {
+            lds.unit = b * A.row_blocks + at / n;
+            lds.first = at % n;
         }
         seen += sum;
-        if (seen * A.row_blocks > begin) break;
     }
     __syncthreads();
     int unit = __builtin_amdgcn_readfirstlane(lds.unit);
@@ -597,7 +577,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
 
     const Lane lane(l);
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
-    int64_t at = begin;
+    int at = begin;
     while (at < end) {
         const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
         const int len = __builtin_amdgcn_readfirstlane(clamp_len(A, b));
@@ -606,7 +586,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
             ++unit;
             continue;
         }
-        const int last = int(end - at < n - first ? first + (end - at) : n);
+        const int last = min(first + (end - at), n);
         const bool whole = first == 0 && last == n;
         const int slot = first == 0 ? unit : units + wg;
         Sink sink;
@@ -614,17 +594,16 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
         sink.first_row = 32 * kRW * blk;
         sink.row0 = int64_t(b) * unit_rows + sink.first_row;
         sink.rows = min(32 * kRW, unit_rows - sink.first_row);
-        sink.part = A.part + size_t(slot) * kGroups * 4 * 32 * kRW;
+        sink.part = A.part + size_t(slot) * kMlaLatent * 32 * kRW;
         sink.ml = A.part_ml + size_t(slot) * 2 * 32 * kRW;
-        sink.stride = 32 * kRW;
+        sink.bad = A.bad + slot;
         if (first == 0 && threadIdx.x == 0) {
             // the workgroups that hold this unit's later pieces
-            const int64_t stop = at + n;
             A.meta[2 * unit] = sink.final ? -1 : wg;
-            A.meta[2 * unit + 1] = int((stop - 1) / per);
+            A.meta[2 * unit + 1] = (at + n - 1) / per;
         }
-        piece<kRW, true>(A, lds, lane, Source{A.table + int64_t(b) * A.table_width, len}, first,
-                         last, sink);
+        piece<kRW, true>(A, lds, lane, Source{A.table + int64_t(b) * A.table_width, len}, first, last,
+                         sink);
         at += last - first;
         first = 0;
         ++unit;
@@ -637,105 +616,79 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
     __shared__ __attribute__((aligned(256))) Lds lds;
     const int l = threadIdx.x & 63, wg = blockIdx.x;
     const Lane lane(l);
-    const int64_t rows = int64_t(A.batch) * A.tokens * A.heads;
+    const int rows = A.batch * A.tokens * A.heads;
     const int n = tiles_of(A.prefix_len);
-    const int64_t total = int64_t(A.prefix_units) * n;
-    int64_t at = A.prefix_per * wg;
-    const int64_t end = min(at + A.prefix_per, total);
+    const int total = A.prefix_units * n;
+    int at = A.prefix_per * wg;
+    const int end = min(at + A.prefix_per, total);
+    if (threadIdx.x == 0) lds.bad = 0;
     while (at < end) {
-        const int unit = int(at / n), first = int(at - int64_t(unit) * n);
-        const int last = int(end - at < n - first ? first + (end - at) : n);
+        const int unit = at / n, first = at - unit * n;
+        const int last = min(first + (end - at), n);
         const int slot = first == 0 ? unit : A.prefix_units + wg;
         Sink sink;
         sink.final = false;
         sink.first_row = 0;
         sink.row0 = int64_t(unit) * 32 * kRW;
-        sink.rows = int(min(int64_t(32 * kRW), rows - sink.row0));
-        sink.part = A.pre_part + size_t(slot) * kGroups * 4 * 32 * kRW;
+        sink.rows = min(32 * kRW, rows - unit * 32 * kRW);
+        sink.part = A.pre_part + size_t(slot) * kMlaLatent * 32 * kRW;
         sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRW;
-        sink.stride = 32 * kRW;
+        sink.bad = A.pre_bad + slot;
         piece<kRW, false>(A, lds, lane, Source{A.prefix_table, A.prefix_len}, first, last, sink);
         at += last - first;
     }
 }
 
-// Joins the partial sums of 32 query rows of a unit, 64 channels a workgroup.
-// Where there are several new tokens it also looks at the rows of the tiles
-// that some of them do not see: a latent value that is infinite or NaN makes
-// that channel NaN for the queries that see it (its score is infinite or NaN
-// too), and the products left it out.
+// Joins the partial sums of a query row, a wave per row (eight channels a lane).
+// Where a sequence's last tiles held infinities or NaN it also looks at the
+// rows that not all of several new tokens see: such a value makes its channel
+// NaN for the queries that see it (their score is infinite or NaN too), and the
+// products left it out.
 __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeArgs A) {
-    __shared__ int bad_s;
-    const int unit = blockIdx.x / A.row_waves, sub = blockIdx.x % A.row_waves;
-    const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
+    const int l = threadIdx.x & 63;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
+    const int row = blockIdx.x * (kThreads / 64) + wave_id();
+    if (row >= A.batch * unit_rows) return;
+    const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
     const int stride = 32 * A.row_waves;
-    const int lr = 32 * sub + int(threadIdx.x & 31);     // row in the unit's block
-    const int urow = stride * blk + lr;                  // row in the sequence
-    const int len = clamp_len(A, b);
-    const bool any = len > 0;
-    const int g0 = any ? A.meta[2 * unit] : -1, g1 = any ? A.meta[2 * unit + 1] : -2;
-    const int32_t* table = A.table + int64_t(b) * A.table_width;
-    const int from = max(len - (A.tokens - 1), 0) / kTile * kTile;
-    const int cg0 = blockIdx.y * 16 + 2 * int(threadIdx.x >> 5);
-    bool bad = false;
-    if (A.tokens > 1) {
-        for (int k = from + int(threadIdx.x >> 3); k < len; k += kThreads / 8) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(
-                cached_row(A, table, k) + 64 * blockIdx.y + 8 * (threadIdx.x & 7));
-            bad |= (nonfinite_bits(x[0]) | nonfinite_bits(x[1]) | nonfinite_bits(x[2]) |
-                    nonfinite_bits(x[3])) != 0;
-        }
-        if (threadIdx.x == 0) bad_s = 0;
-        __syncthreads();
-        if (bad) bad_s = 1;
-        __syncthreads();
-        bad = bad_s != 0;
-    }
-    const bool done = any && g0 < 0;                     // already written
-    if (urow >= unit_rows || (done && !bad)) return;
+    const int blk = urow / stride, lr = urow - blk * stride;     // row in the unit
+    const int unit = b * A.row_blocks + blk;
+    const int len = __builtin_amdgcn_readfirstlane(clamp_len(A, b));
+    int np = 0, g0 = 0;                                  // private pieces, first workgroup
+    bool done = false;                                   // already written
     u32x4 nan = {};                                      // 0xffff where a channel is NaN
-    if (bad) {
-        const int limit = len - (A.tokens - 1 - urow / A.heads);
-        for (int k = from; k < limit; ++k) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(cached_row(A, table, k) + 4 * cg0);
+    if (len > 0) {
+        g0 = __builtin_amdgcn_readfirstlane(A.meta[2 * unit]);
+        done = g0 < 0;
+        np = done ? 0 : __builtin_amdgcn_readfirstlane(A.meta[2 * unit + 1]) - g0 + 1;
+        int bad = A.bad[unit];
+        for (int i = 1 + l; i < np; i += 64) bad |= A.bad[units + g0 + i];
+        if (__any(bad)) {
+            const int32_t* table = A.table + int64_t(b) * A.table_width;
+            const int from = max(len - (A.tokens - 1), 0) / kTile * kTile;
+            const int limit = len - (A.tokens - 1 - urow / A.heads);
+            for (int k = from; k < limit; ++k) {
+                const u32x4 x = *reinterpret_cast<const u32x4*>(cached_row(A, table, k) + 8 * l);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) nan[i] |= (nonfinite_bits(x[i]) >> 15) * 0xffffu;
+                for (int i = 0; i < 4; ++i) nan[i] |= (nonfinite_bits(x[i]) >> 15) * 0xffffu;
+            }
         }
     }
-    const int64_t row = int64_t(b) * unit_rows + urow;
-    u32x4* const o = reinterpret_cast<u32x4*>(A.o + row * kMlaLatent + 4 * cg0);
+    u32x4* const o = reinterpret_cast<u32x4*>(A.o + int64_t(row) * kMlaLatent + 8 * l);
     if (done) {
-        *o |= nan;
+        if (__any((nan[0] | nan[1] | nan[2] | nan[3]) != 0)) *o |= nan;
         return;
     }
-    const int np = any ? g1 - g0 + 1 : 0;                // private pieces
     // prefix pieces of this row
-    int pn = 0, pu = 0, pr = 0;
-    int64_t pg0 = 0;
-    if (A.prefix_len) {
-        const int n = tiles_of(A.prefix_len), prows = 32 * A.prefix_waves;
-        pu = int(row / prows);
-        pr = int(row - int64_t(pu) * prows);
-        pg0 = int64_t(pu) * n / A.prefix_per;
-        pn = int((int64_t(pu + 1) * n - 1) / A.prefix_per - pg0) + 1;
-    }
+    int pn = 0, pu = 0, pr = 0, pg0 = 0;
     const int pstride = 32 * A.prefix_waves;
-    auto slot_of = [&](int i, const float*& part, const float*& ml, int& st, int& r) {
-        if (i < np) {
-            const size_t s = i == 0 ? size_t(unit) : size_t(units) + g0 + i;
-            part = A.part + s * kGroups * 4 * stride;
-            ml = A.part_ml + s * 2 * stride;
-            st = stride;
-            r = lr;
-        } else {
-            const size_t s = i == np ? size_t(pu) : size_t(A.prefix_units) + pg0 + (i - np);
-            part = A.pre_part + s * kGroups * 4 * pstride;
-            ml = A.pre_ml + s * 2 * pstride;
-            st = pstride;
-            r = pr;
-        }
-    };
+    if (A.prefix_len) {
+        const int n = tiles_of(A.prefix_len);
+        pu = row / pstride;
+        pr = row - pu * pstride;
+        pg0 = pu * n / A.prefix_per;
+        pn = (pu * n + n - 1) / A.prefix_per - pg0 + 1;
+    }
     // eight pieces' sums at a time, all loads before their use
     constexpr int kN = 8;
     const int n = np + pn;
@@ -746,13 +699,15 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
         f32x4 x[kN][2];
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-            const float *part, *pml;
-            int st, r;
-            slot_of(min(i0 + e, n - 1), part, pml, st, r);
-            ml[e] = *reinterpret_cast<const f32x2*>(pml + 2 * r);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                x[e][k] = *reinterpret_cast<const f32x4*>(part + (size_t(cg0 + k) * st + r) * 4);
+            const int i = min(i0 + e, n - 1);
+            const bool own = i < np;
+            const int slot = own ? (i == 0 ? unit : units + g0 + i)
+                                 : (i == np ? pu : A.prefix_units + pg0 + (i - np));
+            const size_t at = size_t(slot) * (own ? stride : pstride) + (own ? lr : pr);
+            ml[e] = *reinterpret_cast<const f32x2*>((own ? A.part_ml : A.pre_ml) + 2 * at);
+            const float* part = (own ? A.part : A.pre_part) + at * kMlaLatent + 8 * l;
+            x[e][0] = *reinterpret_cast<const f32x4*>(part);
+            x[e][1] = *reinterpret_cast<const f32x4*>(part + 4);
         }
         float most = top;
 #pragma unroll
@@ -776,13 +731,10 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
     const float inv = inverse(total);
     u32x4 out;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const f32x2 v = {sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv};
-        out[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-    }
+    for (int k = 0; k < 4; ++k)
+        out[k] = pack2(sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv);
     *o = out | nan;
-    if (A.lse && blockIdx.y == 0 && threadIdx.x < 32)
-        A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
+    if (A.lse && l == 0) A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
 }
 
 template <int kRW>
@@ -792,7 +744,7 @@ void launch_private(const MlaDecodeArgs& A, hipStream_t stream) {
 
 template <int kRW>
 void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
-    const int64_t total = int64_t(A.prefix_units) * ((A.prefix_len + kTile - 1) / kTile);
+    const int total = A.prefix_units * ((A.prefix_len + kTile - 1) / kTile);
     mla_prefix_kernel<kRW><<<dim3(unsigned((total + A.prefix_per - 1) / A.prefix_per)),
                              dim3(kThreads), 0, stream>>>(A);
 }
@@ -809,8 +761,8 @@ hipError_t launch_mla_decode(const MlaDecodeArgs& A, hipStream_t stream) {
     else if (A.row_waves == 2) launch_private<2>(A, stream);
     else launch_private<1>(A, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    mla_combine_kernel<<<dim3(unsigned(A.batch * A.row_blocks * A.row_waves), 8), dim3(kThreads), 0,
-                         stream>>>(A);
+    const int rows = A.batch * A.tokens * A.heads;
+    mla_combine_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
