@@ -52,8 +52,11 @@ struct Tile {
     unsigned char pe[kTile * kPeBytes];
 };
 
+constexpr int kShare = 12;   // query operands exchanged at a time
+
 struct Lds {
     Tile tile[4];
+    u32x4 q[kShare][64];
     float ml[4][2][32];     // (mu, l) of each wave's rows
     int scan[8];
     int unit, first;        // where this workgroup's piece begins
@@ -208,12 +211,11 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 
 // Four channels of a row, and a row's statistics.
-__device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x,
-                                     float inv) {
+__device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x) {
     if (S.final) {
         if (row < S.rows)
             *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
-                u32x2{pack2(x[0] * inv, x[1] * inv), pack2(x[2] * inv, x[3] * inv)};
+                u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
     } else {
         *reinterpret_cast<f32x4*>(S.part + size_t(row) * kMlaLatent + ch) = x;
     }
@@ -315,6 +317,20 @@ __device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const S
         *sink.bad = lds.bad;
         lds.bad = 0;
     }
+    // each lane: its row's part of every key wave's sums, and the quotient
+    float f[kKW], total = 0.f, top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kKW; ++k) top = fmaxf(top, lds.ml[k * kRW + rw][0][l & 31]);
+#pragma unroll
+    for (int k = 0; k < kKW; ++k) {
+        const float x = lds.ml[k * kRW + rw][0][l & 31];
+        f[k] = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
+        total = fmaf(lds.ml[k * kRW + rw][1][l & 31], f[k], total);
+    }
+    if (kw == 0 && l < 32) put_ml(A, sink, 32 * rw + l, top, total);
+    const float inv = sink.final ? inverse(total) : 1.f;
+#pragma unroll
+    for (int k = 0; k < kKW; ++k) f[k] *= inv;
     const uint32_t mine = lds_addr(&lds.tile[w]) + (l & 31) * kStride + 16 * (l >> 5);
     unrolled<2>([&](auto ph) {
         constexpr int phase = decltype(ph)::value;
@@ -324,24 +340,26 @@ __device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const S
             acc_store<32 * phase + n, 128 * (n / 4) + 32 * (n % 4)>(mine);
         });
         raw_barrier();
-#pragma unroll 4
-        for (int i = 0; i < kRows; ++i) {
-            const int r = kw * kRows + i;
-            float top = lds.ml[rw][0][r];
+        constexpr int kR = 8;   // rows at a time, all reads before their use
+#pragma unroll 1
+        for (int r0 = kw * kRows; r0 < (kw + 1) * kRows; r0 += kR) {
+            f32x4 x[kR][kKW];
 #pragma unroll
-            for (int k = 1; k < kKW; ++k) top = fmaxf(top, lds.ml[k * kRW + rw][0][r]);
-            float total = 0.f;
-            f32x4 sum = zero4();
+            for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int k = 0; k < kKW; ++k) {
-                const float x = lds.ml[k * kRW + rw][0][r];
-                const float f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - top);
-                total = fmaf(lds.ml[k * kRW + rw][1][r], f, total);
-                sum += *reinterpret_cast<const f32x4*>(
-                           reinterpret_cast<const char*>(&lds.tile[k * kRW + rw]) + r * kStride + 16 * l) * f;
+                for (int k = 0; k < kKW; ++k)
+                    x[i][k] = *reinterpret_cast<const f32x4*>(
+                        reinterpret_cast<const char*>(&lds.tile[k * kRW + rw]) + (r0 + i) * kStride + 16 * l);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                f32x4 sum = zero4();
+#pragma unroll
+                for (int k = 0; k < kKW; ++k) {
+                    const float fk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f[k]), r0 + i));
+                    sum += x[i][k] * fk;
+                }
+                put4(A, sink, 32 * rw + r0 + i, 256 * phase + 4 * l, sum);
             }
-            put4(A, sink, 32 * rw + r, 256 * phase + 4 * l, sum, inverse(total));
-            if (phase == 0 && l == 0) put_ml(A, sink, 32 * rw + r, top, total);
         }
     });
     raw_barrier();   // the next piece refills the tiles
@@ -369,25 +387,54 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
     // this wave's part of tile t.  (A tile behind the last one is fetched too, as
     // zeros: the number of transfers in flight is the same in every step.)
     auto first_row = [&](int t, int n) { return t * kTile + 8 * (rw * kIssue + n); };
-    int page = page_of(A, src, first_row(t0 + kw, 0));
+    int page[kIssue];   // of the next tile to fetch
+    auto pages = [&](int t) {
+#pragma unroll
+        for (int n = 0; n < kIssue; ++n) page[n] = page_of(A, src, first_row(t, n));
+    };
     auto issue = [&](int t, int buf) {
-#pragma unroll 1
+#pragma unroll
         for (int n = 0; n < kIssue; ++n) {
-            const Fetch f(A, page, first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
-            // the page of the fetch after this one
-            page = page_of(A, src, n + 1 < kIssue ? first_row(t, n + 1) : first_row(t + kKW, 0));
+            const Fetch f(A, page[n], first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
 #pragma unroll
             for (int x = 0; x < 9; ++x) f.issue(x, l);
         }
+        pages(t + kKW);
     };
     constexpr int kLead = kBuf > 1 ? kBuf - 1 : 1;   // tiles fetched ahead of the loop
+    pages(t0 + kw);
 #pragma unroll 1
     for (int d = 0; d < kLead; ++d) issue(t0 + d * kKW + kw, d);
+    // key waves have the same query rows: each loads its part of the operands
+    // and they exchange them (the loads are what is slow: 32 rows apart)
+    constexpr int kOwn = 36 / kKW;
     bf16x8 qf[36];
+    if constexpr (kKW == 1) {
 #pragma unroll
-    for (int m = 0; m < 36; ++m)
-        qf[m] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qrow + 16 * m + 8 * g));
-    unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
+        for (int m = 0; m < 36; ++m)
+            qf[m] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qrow + 16 * m + 8 * g));
+        unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
+    } else {
+        u32x4 mine[kOwn];
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m)
+            mine[m] = *reinterpret_cast<const u32x4*>(qrow + 16 * (kw * kOwn + m) + 8 * g);
+        unrolled<256>([](auto q) { acc_clear<decltype(q)::value>(); });
+        constexpr int kEach = kShare / 4;   // operands of a wave at a time
+#pragma unroll
+        for (int r = 0; r < kOwn / kEach; ++r) {
+            raw_barrier();
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) lds.q[w * kEach + e][l] = mine[r * kEach + e];
+            raw_barrier();
+#pragma unroll
+            for (int k = 0; k < kKW; ++k)
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    qf[k * kOwn + r * kEach + e] =
+                        __builtin_bit_cast(bf16x8, lds.q[(k * kRW + rw) * kEach + e][l]);
+        }
+    }
     // the queries have arrived before the loop: no wait of the compiler's own
     // stands in it
 #pragma unroll
