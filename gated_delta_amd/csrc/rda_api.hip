@@ -1229,7 +1229,8 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
 
 size_t rda_verify_drafts_workspace_bytes(int32_t batch, int32_t vocab) {
     if (batch < 0 || vocab < 1) return 0;
-    return align256(size_t(batch) * verify_chunks(vocab) * 2 * sizeof(double));
+    return align256(size_t(batch) * verify_chunks(vocab) * 2 * sizeof(double)) +
+           align256(size_t(batch) * 2 * sizeof(int32_t));
 }
 
 rda_status rda_verify_drafts(const float* target, int64_t target_stride, const float* draft,
@@ -1277,6 +1278,9 @@ rda_status rda_verify_drafts(const float* target, int64_t target_stride, const f
     A.accept = accept;
     A.out = out_tokens;
     A.sums = static_cast<double*>(workspace);
+    A.choice = reinterpret_cast<int32_t*>(
+        static_cast<unsigned char*>(workspace) +
+        align256(size_t(batch) * verify_chunks(vocab) * 2 * sizeof(double)));
     return launch_verify(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
 }
 

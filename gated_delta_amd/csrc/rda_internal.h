@@ -387,6 +387,7 @@ struct VerifyArgs {
     int32_t* accept;             // [B]
     int32_t* out;                // [B, D + 1]
     double* sums;                // workspace: [B, chunks, 2]
+    int32_t* choice;             // workspace: [B, 2]
 };
 int32_t verify_chunks(int32_t vocab);
 hipError_t launch_verify(const VerifyArgs& A, hipStream_t stream);

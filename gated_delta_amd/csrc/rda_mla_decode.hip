@@ -212,10 +212,10 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 
 // Four channels of a row, and a row's statistics.
 __device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x) {
+    if (row >= S.rows) return;
     if (S.final) {
-        if (row < S.rows)
-            *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
-                u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
+        *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
+            u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
     } else {
         *reinterpret_cast<f32x4*>(S.part + size_t(row) * kMlaLatent + ch) = x;
     }

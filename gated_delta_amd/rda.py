@@ -10,6 +10,7 @@ library is not built, the first call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -443,11 +444,20 @@ class _On:
             torch.cuda.set_device(self.before)
 
 
-def _stream_on(dev: torch.device, stream) -> ctypes.c_void_p:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(dev: torch.device, stream) -> int:
     """The given stream, or the current one of the tensors' device."""
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(dev.index)
         stream = torch.cuda.current_stream(dev)
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
@@ -457,18 +467,17 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    width, want = 1, []
-    for n in reversed(shape[1:]):
-        want.insert(0, width)
-        width *= n
-    for n, have, need in zip(shape[1:], t.stride()[1:], want):
-        if n > 1 and have != need:
+    stride, width = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        n = shape[i]
+        if n > 1 and stride[i] != width:
             raise ValueError(f"{name}: the values of a row must be contiguous")
-    return t.stride(0) if shape[0] > 1 else width
+        width *= n
+    return stride[0] if shape[0] > 1 else width
 
 
 def _offsets(cu, name: str, total: int, device) -> Optional[torch.Tensor]:
@@ -519,14 +528,15 @@ def rda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale
     if lse is not None:
         _need(lse, "lse", torch.float32, (Tq, H), dev)
     with _On(dev):
-        st = lib_.rda_mla_prefill(_ptr(q), qs, _ptr(kv), ks, _ptr(k_pe), ps, _ptr(cq), _ptr(ck),
+        st = lib_.rda_mla_prefill(_addr(q), qs, _addr(kv), ks, _addr(k_pe), ps, _addr(cq), _addr(ck),
                                   1 if cq is None else cq.numel() - 1, Tq, Tk, H, float(scale),
-                                  int(bool(causal)), _ptr(o), _ptr(lse), _stream_on(dev, stream))
+                                  int(bool(causal)), _addr(o), _addr(lse), _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_mla_prefill")
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
 def rda_mla_decode_workspace_bytes(batch: int, tokens: int, num_heads: int,
                                    prefix_len: int = 0) -> int:
     return int(_load().rda_mla_decode_workspace_bytes(int(batch), int(tokens), int(num_heads),
@@ -581,13 +591,13 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, H), dev)
     if workspace is None:
-        workspace = _workspace(lib_.rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)),
+        workspace = _workspace(rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)),
                                dev, stream)
     with _On(dev):
-        st = lib_.rda_mla_decode(_ptr(q), _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
-                                 _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
-                                 _ptr(prefix_table) if prefix_len > 0 else None, prefix_len, B, T,
-                                 H, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+        st = lib_.rda_mla_decode(_addr(q), _addr(cache), page_stride, cache.shape[0], cache.shape[1],
+                                 _addr(block_table), block_table.shape[1], _addr(kv_lens),
+                                 _addr(prefix_table) if prefix_len > 0 else None, prefix_len, B, T,
+                                 H, float(scale), _addr(o), _addr(lse), _addr(workspace),
                                  workspace.numel() * workspace.element_size(),
                                  _stream_on(dev, stream))
     if st != 0:
@@ -633,15 +643,16 @@ def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     if weight is not None:
         _need(weight, "weight", torch.float32, (RDA_MLA_LATENT,), dev)
     with _On(dev):
-        st = lib_.rda_mla_append(_ptr(kv), stride, _ptr(weight), float(eps), _ptr(cu), N, T,
-                                 _ptr(kv_lens), _ptr(block_table), block_table.shape[1],
-                                 _ptr(cache), page_stride, cache.shape[0], cache.shape[1],
+        st = lib_.rda_mla_append(_addr(kv), stride, _addr(weight), float(eps), _addr(cu), N, T,
+                                 _addr(kv_lens), _addr(block_table), block_table.shape[1],
+                                 _addr(cache), page_stride, cache.shape[0], cache.shape[1],
                                  _stream_on(dev, stream))
     if st != 0:
         raise RdaError(st, "rda_mla_append")
     return cache
 
 
+@functools.lru_cache(maxsize=256)
 def rda_verify_drafts_workspace_bytes(batch: int, vocab: int) -> int:
     return int(_load().rda_verify_drafts_workspace_bytes(int(batch), int(vocab)))
 
@@ -694,11 +705,11 @@ def rda_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
         out_tokens = torch.empty((B, T), dtype=torch.int32, device=dev)
     _need(out_tokens, "out_tokens", torch.int32, (B, T), dev)
     if workspace is None:
-        workspace = _workspace(lib_.rda_verify_drafts_workspace_bytes(B, V), dev, stream)
+        workspace = _workspace(rda_verify_drafts_workspace_bytes(B, V), dev, stream)
     with _On(dev):
-        st = lib_.rda_verify_drafts(_ptr(target), ts, _ptr(draft) if T > 1 else None, ds,
-                                    _ptr(draft_tokens), _ptr(uniforms), _ptr(num_drafts), B, T - 1,
-                                    V, _ptr(accept), _ptr(out_tokens), _ptr(workspace),
+        st = lib_.rda_verify_drafts(_addr(target), ts, _addr(draft) if T > 1 else None, ds,
+                                    _addr(draft_tokens), _addr(uniforms), _addr(num_drafts), B, T - 1,
+                                    V, _addr(accept), _addr(out_tokens), _addr(workspace),
                                     workspace.numel() * workspace.element_size(),
                                     _stream_on(dev, stream))
     if st != 0:
