@@ -80,7 +80,7 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
     A.row_waves = unit_rows > 64 ? 4 : unit_rows > 32 ? 2 : 1;
     A.row_blocks = int32_t((unit_rows + 32 * A.row_waves - 1) / (32 * A.row_waves));
-    A.min_tiles = 4;
+    A.min_tiles = 4;   // (and no more than an average unit has: see the kernel)
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* p = ws ? ws + at : nullptr;

@@ -64,10 +64,16 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16& s) {
 // compiler wait for every transfer in flight before any LDS read (it cannot
 // tell the buffers apart), which would end the prefetch; here the waits are
 // the caller's (wait_vm and a barrier before the first read).  It writes M0,
-// which nothing else in these kernels uses.
+// which nothing else in these kernels uses.  kOnce: for memory that is read
+// once (a non-temporal load).
+template <bool kOnce = false>
 __device__ __forceinline__ void dma16_at(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(lds), "v"(off), "s"(base) : "memory");
+    if constexpr (kOnce)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                     ::"s"(lds), "v"(off), "s"(base) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 // The same with an address of each lane's own.

@@ -150,12 +150,15 @@ struct Fetch {
             A.cache + int64_t(page) * A.page_stride +
             int64_t(k & ((1 << A.page_shift) - 1)) * kMlaRow);
     }
-    // transfer i of 0..8
+    // transfer i of 0..8.  kOnce: the latent parts pass the caches by, where one
+    // workgroup reads a row and no other (256 sequences of 4352 rows: 6.1
+    // instead of 5.3 TB/s; a row's last 128 bytes share a line with the next).
+    template <bool kOnce>
     __device__ __forceinline__ void issue(int i, int lane_id) const {
         const char* const zeros = reinterpret_cast<const char*>(kZeros);
         const int l = here(lane_id);
         if (i < 8) {
-            dma16_at(i < valid ? base + i * kRowBytes : zeros, (16 * (l ^ (group & 1))) ^ (32 * i),
+            dma16_at<kOnce>(i < valid ? base + i * kRowBytes : zeros, (16 * (l ^ (group & 1))) ^ (32 * i),
                      lds + (group * 8 + i) * kLatBytes);
         } else {
             const int r = l >> 3, j = (l & 7) ^ ((4 * group + (r >> 1)) & 7);
@@ -397,7 +400,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds& lds, const La
         for (int n = 0; n < kIssue; ++n) {
             const Fetch f(A, page[n], first_row(t, n), end, rw * kIssue + n, group_lds + buf * kTileBytes);
 #pragma unroll
-            for (int x = 0; x < 9; ++x) f.issue(x, l);
+            for (int x = 0; x < 9; ++x) f.template issue<kCausal>(x, l);
         }
         pages(t + kKW);
     };
@@ -601,7 +604,9 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     }
     total *= A.row_blocks;
     const int share = (total + kMlaWorkgroups - 1) / kMlaWorkgroups;
-    const int per = share > A.min_tiles ? share : A.min_tiles;
+    // (short sequences are better spread than put one behind the other)
+    const int units = A.batch * A.row_blocks;
+    const int per = max(share, min(A.min_tiles, (total + units - 1) / units));
     if (int64_t(per) * wg >= total) return;
     const int begin = per * wg, end = min(begin + per, total);
     for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
@@ -623,7 +628,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     int first = __builtin_amdgcn_readfirstlane(lds.first);
 
     const Lane lane(l);
-    const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
+    const int unit_rows = A.tokens * A.heads;
     int at = begin;
     while (at < end) {
         const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
