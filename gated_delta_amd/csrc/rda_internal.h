@@ -327,8 +327,10 @@ struct MlaPrefillArgs {
     float* lse;                // [Tq, H] or nullptr
 };
 // Query-tile slots of a packed batch (an upper bound on its tiles).
-int64_t mla_prefill_slots(int32_t total_q, int32_t num_seqs);
+int64_t mla_prefill_slots(int32_t total_q, int32_t num_seqs);        // 128 queries
+int64_t mla_prefill_wide_slots(int32_t total_q, int32_t num_seqs);   // 256 queries
 hipError_t launch_mla_prefill(const MlaPrefillArgs& A, hipStream_t stream);
+hipError_t launch_mla_prefill_wide(const MlaPrefillArgs& A, hipStream_t stream);
 
 // Absorbed latent attention over a paged cache of latent rows.
 constexpr int kMlaWorkgroups = 256;   // one per CU: its tiles fill a CU's LDS

@@ -47,6 +47,12 @@ __device__ __forceinline__ bf16x8 finite_only(bf16x8 x) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
+// Two values as packed bf16 (the first in the low half), rounded to nearest.
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+    const f32x2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 // 8 consecutive accumulator registers as one bf16 MFMA operand.
 template <int kFrom>
 __device__ __forceinline__ bf16x8 pack8(const f32x16& s) {
@@ -109,14 +115,6 @@ __device__ __forceinline__ u32x2 lds_read_tr8(uint32_t a) {
 // wave's own LDS accesses are done (lgkmcnt), nothing moves across it.
 __device__ __forceinline__ void raw_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// Consecutive pieces of [0, n) for the 8 XCDs: workgroups go to the XCDs in
-// turn by their index, and each XCD has its own L2, so work that reads the
-// same memory gets indexes that are 8 apart.
-__device__ __forceinline__ int xcd_order(int id, int n) {
-    const int x = id & 7, per = n >> 3, extra = n & 7;
-    return x * per + (x < extra ? x : extra) + (id >> 3);
 }
 
 }  // namespace rda

@@ -28,6 +28,7 @@
 
 #include "rda_internal.h"
 #include "rda_mla.h"
+#include "rda_mla_acc.h"
 
 namespace rda {
 namespace {
@@ -208,17 +209,12 @@ struct Sink {
     int32_t* bad;      // set where the last tiles held infinities or NaN
 };
 
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-    const f32x2 v = {x, y};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
-
 // Four channels of a row, and a row's statistics.
 __device__ __forceinline__ void put4(const MlaDecodeArgs& A, const Sink& S, int row, int ch, f32x4 x) {
     if (row >= S.rows) return;
     if (S.final) {
         *reinterpret_cast<u32x2*>(A.o + (S.row0 + row) * kMlaLatent + ch) =
-            u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
+            u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     } else {
         *reinterpret_cast<f32x4*>(S.part + size_t(row) * kMlaLatent + ch) = x;
     }
@@ -234,70 +230,6 @@ __device__ __forceinline__ void put_ml(const MlaDecodeArgs& A, const Sink& S, in
 }
 
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
-
-// O^T of a wave: 16 blocks of 32 channels, block b in the accumulation
-// registers a[16 b] .. a[16 b + 15], written and read by the statements below
-// only.  The compiler is not told that they hold values (left to it, a sum that
-// fills that whole file is copied to memory and back around every branch), but
-// that every statement may change them, so it keeps nothing of its own there;
-// the scores' products, which it would place there too, have ordinary
-// registers.  It does not see matrix products in here either: each waits the
-// two states that ordinary arithmetic needs before one reads its result
-// (s_nop 1), and settle / scores_done stand before a result is read.
-#define RDA_A10(t) "a" #t "0", "a" #t "1", "a" #t "2", "a" #t "3", "a" #t "4", "a" #t "5", \
-                   "a" #t "6", "a" #t "7", "a" #t "8", "a" #t "9"
-#define RDA_ALL_ACC RDA_A10(), RDA_A10(1), RDA_A10(2), RDA_A10(3), RDA_A10(4), RDA_A10(5),    \
-    RDA_A10(6), RDA_A10(7), RDA_A10(8), RDA_A10(9), RDA_A10(10), RDA_A10(11), RDA_A10(12),    \
-    RDA_A10(13), RDA_A10(14), RDA_A10(15), RDA_A10(16), RDA_A10(17), RDA_A10(18), RDA_A10(19),\
-    RDA_A10(20), RDA_A10(21), RDA_A10(22), RDA_A10(23), RDA_A10(24), "a250", "a251", "a252",  \
-    "a253", "a254", "a255"
-
-template <int kN, typename F>
-__device__ __forceinline__ void unrolled(F f) {
-    if constexpr (kN > 0) {
-        unrolled<kN - 1>(f);
-        f(std::integral_constant<int, kN - 1>{});
-    }
-}
-
-template <int kReg>
-__device__ __forceinline__ void acc_clear() {
-    asm volatile("v_accvgpr_write_b32 a[%0], 0" ::"n"(kReg) : RDA_ALL_ACC);
-}
-template <int kReg>
-__device__ __forceinline__ void acc_scale(float f) {
-    float t;
-    asm volatile("v_accvgpr_read_b32 %0, a[%2]\n\tv_mul_f32 %0, %1, %0\n\tv_accvgpr_write_b32 a[%2], %0"
-                 : "=&v"(t) : "v"(f), "n"(kReg) : RDA_ALL_ACC);
-}
-// Registers 4 n .. 4 n + 3 to LDS byte address `at` + kOffset (the caller waits).
-template <int kN, int kOffset>
-__device__ __forceinline__ void acc_store(uint32_t at) {
-    asm volatile("ds_write_b128 %0, a[%1:%2] offset:%3"
-                 ::"v"(at), "n"(4 * kN), "n"(4 * kN + 3), "n"(kOffset) : "memory", RDA_ALL_ACC);
-}
-template <int kBlock>
-__device__ __forceinline__ void acc_product(bf16x8 a, bf16x8 b) {
-    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
-                 ::"v"(a), "v"(b), "n"(16 * kBlock), "n"(16 * kBlock + 15) : RDA_ALL_ACC);
-}
-// Longer than the last products take to write their registers.
-__device__ __forceinline__ void settle() {
-    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: RDA_ALL_ACC);
-}
-
-// A chain of products for the scores.
-__device__ __forceinline__ void scores_first(f32x16& d, bf16x8 a, bf16x8 b) {
-    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0"
-                 : "=&v"(d) : "v"(a), "v"(b) : RDA_ALL_ACC);
-}
-__device__ __forceinline__ void scores_next(f32x16& d, bf16x8 a, bf16x8 b) {
-    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
-                 : "+v"(d) : "v"(a), "v"(b) : RDA_ALL_ACC);
-}
-__device__ __forceinline__ void scores_done(f32x16& d) {
-    asm volatile("s_nop 15\n\ts_nop 7" : "+v"(d)::RDA_ALL_ACC);
-}
 
 // A piece's sums to where they go, by way of LDS (the tiles' memory): 256
 // channels at a time, 32 rows a wave, so that they leave row by row; the key
@@ -784,7 +716,7 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
     u32x4 out;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        out[k] = pack2(sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv);
+        out[k] = pack_bf16(sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv);
     *o = out | nan;
     if (A.lse && l == 0) A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
 }

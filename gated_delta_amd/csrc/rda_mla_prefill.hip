@@ -15,6 +15,7 @@
 
 #include "rda_internal.h"
 #include "rda_mla.h"
+#include "rda_mla_tile.h"
 
 namespace rda {
 namespace {
@@ -31,32 +32,6 @@ struct Lds {
     uint16_t Kp[2][kBN * kMlaPe];     // 8 granules a row, j ^ ((r >> 1) & 7)
     uint16_t V[2][kBN * kMlaV];       // 16 granules a row, j ^ ((r & 3) << 2)
 };
-
-struct Seq {
-    int q0, lq, k0, lk;
-};
-
-// The sequence of query slot `slot` and its 128-query tile.  Sequence n owns
-// the slots from cu[n] / 128 + n on: at least ceil(lq / 128) of them.
-__device__ __forceinline__ int find_tile(const MlaPrefillArgs& A, int slot, Seq& s) {
-    int lo = 0;
-    if (A.cu_q) {
-        int hi = A.num_seqs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (A.cu_q[mid] / kBM + mid <= slot) lo = mid; else hi = mid - 1;
-        }
-    }
-    auto part = [&](const int32_t* cu, int total, int& first, int& len) {
-        const int a = cu ? min(max(cu[lo], 0), total) : 0;
-        const int b = cu ? min(max(cu[lo + 1], a), total) : total;
-        first = a;
-        len = b - a;
-    };
-    part(A.cu_q, A.total_q, s.q0, s.lq);
-    part(A.cu_k, A.total_k, s.k0, s.lk);
-    return slot - (s.q0 / kBM + lo);
-}
 
 struct Dma {
     const MlaPrefillArgs& A;
@@ -161,12 +136,14 @@ __device__ __forceinline__ void add_masked_values(const MlaPrefillArgs& A, const
 __global__ __launch_bounds__(kThreads, 2) void mla_prefill_kernel(const MlaPrefillArgs A) {
     __shared__ __attribute__((aligned(256))) Lds lds;
     const int w = wave_id(), l = threadIdx.x & 63, g = l >> 5;
-    // the latest tiles (of a causal prompt: the longest) first
-    const int item = xcd_order(blockIdx.x, A.slots * A.heads);
-    const int h = item / A.slots;
-    Seq S;
-    const int tile = find_tile(A, A.slots - 1 - (item - h * A.slots), S);
-    if (tile < 0 || tile * kBM >= S.lq) return;
+    // the latest queries (of a causal prompt: those with the most keys) of all
+    // heads first, so that the last to start are short (head by head instead:
+    // 4% slower at 8192 tokens and 32 heads); workgroups go to the 8 XCDs in
+    // turn, so where 8 divides the heads a head's share an XCD's L2
+    const int h = blockIdx.x % A.heads;
+    PromptTile S;
+    if (!find_tile<kBM>(A, A.slots - 1 - int(blockIdx.x) / A.heads, S)) return;
+    const int tile = S.tile;
     const int off = S.lk - S.lq;
     const int qi = tile * kBM + 32 * w + (l & 31);   // this lane's query
     const int qlast = min(tile * kBM + kBM, S.lq) - 1;
@@ -297,7 +274,25 @@ int64_t mla_prefill_slots(int32_t total_q, int32_t num_seqs) {
     return int64_t(total_q) / kBM + num_seqs;
 }
 
+// The wide kernel halves what each query reads from LDS, but its workgroups are
+// twice as large and one fits a CU: it needs two for every CU, sequences that
+// fill them (512 queries on average) and key ranges over which its longer start
+// and end (about 15 us a workgroup) count little.  Narrow and wide, us: 8192 tokens x 32
+// heads 934 and 858, 4096 x 32 254 and 237, 8 x 1024 over 5120 keys x 16 508
+// and 444; on the other side of the rule, 8 x 1024 x 32 188 and 194, 1024 x 128
+// 80 and 86, 4096 x 16 163 and 169, 32 x 256 over 512 keys x 16 80 and 124.
+static bool prefer_wide(const MlaPrefillArgs& A, int64_t slots) {
+    return slots * A.heads >= 2 * kMlaWorkgroups && A.total_q >= int64_t(512) * A.num_seqs &&
+           A.total_k >= int64_t(2048) * A.num_seqs;
+}
+
 hipError_t launch_mla_prefill(const MlaPrefillArgs& A, hipStream_t stream) {
+    const int64_t wide = mla_prefill_wide_slots(A.total_q, A.num_seqs);
+    if (prefer_wide(A, wide)) {
+        MlaPrefillArgs W = A;
+        W.slots = int32_t(wide);
+        return launch_mla_prefill_wide(W, stream);
+    }
     mla_prefill_kernel<<<dim3(unsigned(A.slots * A.heads)), dim3(kThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
