@@ -100,10 +100,12 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
         // blocks of 128 rows once they fill the chip with long shares, else
         // blocks of 32, whose four waves share out the tiles
         const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
-        A.prefix_waves = (rows + 127) / 128 * tiles >= 8 * kMlaWorkgroups ? 4 : 1;
+        const int64_t blocks = (rows + 127) / 128;
+        A.prefix_waves = blocks * tiles >= 8 * kMlaWorkgroups || 2 * blocks >= kMlaWorkgroups ? 4 : 1;
         A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
         const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
-        A.prefix_per = int32_t(share > 8 ? share : 8);
+        const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
+        A.prefix_per = int32_t(share > least ? share : least);
         A.pre_bad = reinterpret_cast<int32_t*>(
             take((size_t(A.prefix_units) + kMlaWorkgroups) * sizeof(int32_t)));
         const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_waves;

@@ -53,7 +53,8 @@ struct Tile {
     unsigned char pe[kTile * kPeBytes];
 };
 
-constexpr int kShare = 12;   // query operands exchanged at a time
+constexpr int kPieceTiles = 6;   // one more piece takes at least as long as these
+constexpr int kShare = 12;       // query operands exchanged at a time
 
 struct Lds {
     Tile tile[4];
@@ -526,19 +527,51 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
     };
     auto tiles_at = [&](int b) { return b < A.batch ? tiles_of(clamp_len(A, b)) : 0; };
     if (threadIdx.x == 0) lds.bad = 0;
-    const int n0 = tiles_at(threadIdx.x);
+    int n0 = tiles_at(threadIdx.x);
     int before0;
-    const int total0 = block_sum(n0, before0);
+    int total0 = block_sum(n0, before0);
     int total = total0;
     for (int b0 = kThreads; b0 < A.batch; b0 += kThreads) {
         int before;
         total += block_sum(tiles_at(b0 + int(threadIdx.x)), before);
     }
     total *= A.row_blocks;
+    if (total == 0) return;
     const int share = (total + kMlaWorkgroups - 1) / kMlaWorkgroups;
     // (short sequences are better spread than put one behind the other)
     const int units = A.batch * A.row_blocks;
-    const int per = max(share, min(A.min_tiles, (total + units - 1) / units));
+    int per = max(share, min(A.min_tiles, (total + units - 1) / units));
+    // A piece costs a workgroup as much as six tiles or more besides its own
+    // (queries in, sums out), so with no more units than workgroups none takes
+    // pieces of two units if that makes its share at most so much longer.  The
+    // units' tiles are counted up to multiples of `per` then (half a share lost
+    // per unit on average); a whole unit where it is hardly longer.
+    bool apart = false;
+    if (units <= kMlaWorkgroups && share < 1 << 20) {
+        int most = n0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+        if (l == 0) lds.scan[4 + w] = most;
+        __syncthreads();
+        most = __builtin_amdgcn_readfirstlane(
+            max(max(lds.scan[4], lds.scan[5]), max(lds.scan[6], lds.scan[7])));
+        int each = max(A.min_tiles, total / (kMlaWorkgroups - units / 2) + 1);
+        for (int tries = 0; tries < 2 && !apart && each <= max(share, A.min_tiles) + kPieceTiles; ++tries) {
+            if (most <= each + 2) each = most;
+            const int padded = (n0 + each - 1) / each * each;
+            int before;
+            const int sum = block_sum(padded, before);
+            if (sum * A.row_blocks <= each * kMlaWorkgroups) {
+                apart = true;
+                per = each;
+                n0 = padded;
+                before0 = before;
+                total0 = sum;
+                total = sum * A.row_blocks;
+            }
+            each += each / 8 + 1;
+        }
+    }
     if (int64_t(per) * wg >= total) return;
     const int begin = per * wg, end = min(begin + per, total);
     for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
@@ -588,6 +621,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_kernel(const MlaDecode
         }
         piece<kRW, true>(A, lds, lane, Source{A.table + int64_t(b) * A.table_width, len}, first, last,
                          sink);
+        if (apart) break;
         at += last - first;
         first = 0;
         ++unit;
