@@ -73,9 +73,11 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // pointers too.  Returns the bytes.
 //
 // Query rows go in blocks of 32, 64 or 128 (1, 2 or 4 row waves), whichever
-// holds a sequence's rows.  Every workgroup takes an equal share of the tiles,
-// but at least min_tiles: a share that small costs more in partial sums (64 KiB
-// per 32 rows) than in tiles (36 KiB each).
+// holds a sequence's rows.  The kernel gives every workgroup an equal share of
+// the tiles, but at least min_tiles: a share that small costs more in partial
+// sums (64 KiB per 32 rows) than in tiles (36 KiB each).  2 instead of 4: 8 x
+// 270 rows x 80 query rows 26 us for 28, but 7 sequences of 950 rows 22.5 for
+// 20.5 and one of 777 rows 21 for 20.
 size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
     A.row_waves = unit_rows > 64 ? 4 : unit_rows > 32 ? 2 : 1;
@@ -97,7 +99,8 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
     A.prefix_units = 0;
     A.prefix_per = 1;
     if (A.prefix_len > 0 && rows > 0) {
-        // blocks of 128 rows once they fill the chip with long shares, else
+        // blocks of 128 rows once they fill the chip with long shares, or half of it
+        // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
         // blocks of 32, whose four waves share out the tiles
         const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
         const int64_t blocks = (rows + 127) / 128;

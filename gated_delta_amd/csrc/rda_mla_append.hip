@@ -6,7 +6,10 @@
 //            (or x_c as it is), rounded to bf16 once
 //   shared key channels: copied.
 // One wave per token: 16 bytes a lane of the latent, 16 bytes of lanes 0..7
-// for the rest; the sum of squares meets in the wave.
+// for the rest; the sum of squares meets in the wave.  Bound by memory where
+// there are many rows: 32768 rows 14.8 us, 5.1 TB/s read and written; 768 rows
+// 9.7 us, the launch and one latency after the other (offsets, length, page,
+// row).
 #include "rda_internal.h"
 #include "rda_mla.h"
 

@@ -11,6 +11,15 @@
 // a lane owns one query: the D registers of S^T are, rounded to bf16, the B
 // operand of the second product in the order (4g .. 4g+3, 8 + 4g ..) of the
 // keys, which the transposing reads of V follow.  P never leaves registers.
+//
+// Two workgroups share a CU's LDS (two tiles of 40 KiB each), so one's products
+// run beside the other's exponentials.  An operand read from LDS feeds one
+// product of 32 cycles, about as long as the CU's LDS needs for it, so LDS and
+// the matrix cores are equally busy.  Measured: 4096 new tokens of 5 sequences
+// behind 3001 cached ones, 16 heads, 121 us, 427 TFLOP/s; 2048 tokens of 32
+// heads 87 us; 65 tokens 13.9 us.  A few queries over a long context are the
+// weak side: a wave's tile after the other, 2.2 us each (30 queries over 1959
+// keys 70 us).
 #include <type_traits>
 
 #include "rda_internal.h"

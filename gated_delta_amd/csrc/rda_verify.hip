@@ -17,7 +17,9 @@
 // chunks so that a small batch fills the chip too; every workgroup derives r
 // itself, from a few scalars.  The pick kernel, one workgroup per sequence,
 // finds the chunk (each of its waves by itself, up to 64 chunks in one scan)
-// and reads only that again.
+// and reads only that again.  256 sequences of 259840 tokens: 85 us, 6.3 TB/s
+// for the 532 MB of the two rows each; 8 sequences of 32003: 17.9 us, the two
+// launches and a chain of small loads.
 #include <climits>
 #include <cmath>
 

@@ -25,7 +25,9 @@
  * per-channel decay); rda_prologue produces their
  * inputs from the raw projections (short convolution, q/k norm, gates), and
  * rda_output_norm_gate is the block's output norm and gate on the mixer's
- * output.
+ * output.  The layers between the mixer's have rda_mla_prefill, rda_mla_decode
+ * and rda_mla_append (latent attention and its paged cache), and
+ * rda_verify_drafts yields the accept counts that rda_decode_tokens takes.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -588,8 +590,8 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
  *   block_table, cache, page_stride, num_pages, page_tokens
  *               as in rda_mla_decode.  A row whose position or page id is out
  *               of range is not written; nothing else of the cache changes.
- * Two positions that share a page slot (a page listed twice) leave one of
- * the two rows there.
+ * A position that two rows of one call go to (a page listed twice) is left
+ * with values of either.
  */
 rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight, float eps,
                           const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
