@@ -32,6 +32,10 @@ bool overlap(Range x, Range y) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A launch holds fewer than 2^32 threads: with 256 of them a workgroup, fewer
+// than this many workgroups.
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 24;
+
 // Rows of `width` 16-bit values, `stride` values apart: 16-byte rows, and
 // 64 of them within 32-bit byte offsets.
 bool stride_ok(int64_t stride, int64_t width) {
@@ -1078,7 +1082,7 @@ rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int6
         !stride_ok(pe_stride, RDA_MLA_PE))
         return RDA_ERR_SHAPE;
     const int64_t slots = mla_prefill_slots(total_q, num_seqs);
-    if (slots * H > INT32_MAX) return RDA_ERR_SHAPE;
+    if (slots * H >= kMaxWorkgroups) return RDA_ERR_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return RDA_ERR_VALUE;
     if (total_q == 0) return RDA_OK;
     if (!q || !o || (total_k > 0 && (!kv || !k_pe))) return RDA_ERR_NULL;
@@ -1087,7 +1091,7 @@ rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int6
     for (const void* p : {static_cast<const void*>(cu_q), static_cast<const void*>(cu_k),
                           static_cast<const void*>(lse)})
         if (p && !aligned4(p)) return RDA_ERR_ALIGN;
-    const size_t ni = size_t(num_seqs + 1) * 4;
+    const size_t ni = (size_t(num_seqs) + 1) * 4;
     const Range in[] = {rng(q, rows_bytes(total_q, q_stride, H * RDA_MLA_QK)),
                         rng(kv, rows_bytes(total_k, kv_stride, H * RDA_MLA_KV)),
                         rng(k_pe, rows_bytes(total_k, pe_stride, RDA_MLA_PE)),
@@ -1193,7 +1197,8 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
                           const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
                           void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
                           hipStream_t stream) {
-    if (num_seqs < 1 || total_tokens < 0 || (!cu_seqlens && total_tokens % num_seqs))
+    if (num_seqs < 1 || total_tokens < 0 || total_tokens > (1 << 25) ||
+        (!cu_seqlens && total_tokens % num_seqs))
         return RDA_ERR_SHAPE;
     if (!stride_ok(kv_stride, RDA_MLA_ROW)) return RDA_ERR_SHAPE;
     if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
@@ -1209,7 +1214,7 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
         if (p && !aligned4(p)) return RDA_ERR_ALIGN;
     const Range rc = rng(cache, rows_bytes(num_pages, page_stride, int64_t(page_tokens) * RDA_MLA_ROW));
     for (const Range& r : {rng(kv, rows_bytes(total_tokens, kv_stride, RDA_MLA_ROW)),
-                           rng(weight, RDA_MLA_LATENT * 4), rng(cu_seqlens, size_t(num_seqs + 1) * 4),
+                           rng(weight, RDA_MLA_LATENT * 4), rng(cu_seqlens, (size_t(num_seqs) + 1) * 4),
                            rng(kv_lens, size_t(num_seqs) * 4),
                            rng(block_table, size_t(num_seqs) * table_width * 4)})
         if (overlap(rc, r)) return RDA_ERR_ALIAS;

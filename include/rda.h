@@ -511,7 +511,7 @@ rda_status rda_prefill_norm_gate(const void* q, const void* k, const void* v, rd
  *   k_pe    [total_k] rows pe_stride values apart of 64 values (a slice of
  *           the cached rows as it is)
  *           Strides are multiples of 8, at least the row's width and at most
- *           2^24 (RDA_ERR_SHAPE).
+ *           2^24; (total_q / 128 + num_seqs) x H is below 2^24 (RDA_ERR_SHAPE).
  *   cu_q, cu_k  device int32 [num_seqs + 1] offsets of the queries and keys
  *           (trusted as in rda_prefill, never used out of bounds); cu_k NULL:
  *           as cu_q (total_k = total_q); both NULL: one sequence
@@ -580,6 +580,7 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
  * rounded to bf16, and the 64 shared key channels as they are.
  *
  *   kv          [total_tokens] rows kv_stride values apart of 576 bf16 values
+ *               (total_tokens at most 2^25: RDA_ERR_SHAPE)
  *   weight      [512] fp32, or NULL to copy the latent part as it is
  *   eps         finite and >= 0 (RDA_ERR_VALUE)
  *   cu_seqlens  device int32 [num_seqs + 1] offsets of the new tokens, or
