@@ -27,7 +27,7 @@
 //
 // Measured (32 heads, 512 to 8192 rows a sequence): 256 sequences 247 us, 1.25
 // GB of rows at 5.1 TB/s, where a plain read of as much in this order reaches
-// 6.1; 32 sequences of 3 tokens 68 us (2.2 TB/s: 17 tiles a workgroup, about
+// 6.1; 32 sequences of 3 tokens 65 us (2.3 TB/s: 17 tiles a workgroup, about
 // 2 us each with 96 of 128 query rows in use, and 20 us to load queries and to
 // write and join sums); 12288 query rows (128 sequences of 3 tokens) behind 16384
 // shared rows: the prefix 455 us, 963 TFLOP/s.  One sequence of 777 rows takes 18 us, of

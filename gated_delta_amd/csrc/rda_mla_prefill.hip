@@ -7,7 +7,7 @@
 //
 // One workgroup of four waves takes 128 queries of one head, a wave 32 of
 // them, and walks the keys in tiles of 64 that arrive by LDS-DMA one tile
-// ahead.  The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that
+// ahead (three where a workgroup has a CU for itself).  The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that
 // a lane owns one query: the D registers of S^T are, rounded to bf16, the B
 // operand of the second product in the order (4g .. 4g+3, 8 + 4g ..) of the
 // keys, which the transposing reads of V follow.  P never leaves registers.
@@ -16,10 +16,10 @@
 // run beside the other's exponentials.  An operand read from LDS feeds one
 // product of 32 cycles, about as long as the CU's LDS needs for it, so LDS and
 // the matrix cores are equally busy.  Measured: 4096 new tokens of 5 sequences
-// behind 3001 cached ones, 16 heads, 121 us, 427 TFLOP/s; 2048 tokens of 32
+// behind 3001 cached ones, 16 heads, 115 us, 450 TFLOP/s; 2048 tokens of 32
 // heads 87 us; 65 tokens 13.9 us.  A few queries over a long context are the
-// weak side: a wave's tile after the other, 2.2 us each (30 queries over 1959
-// keys 70 us).
+// weak side: a wave's tile after the other, 2 us each, most of it latency
+// (30 queries over 1959 keys 64 us).
 #include <type_traits>
 
 #include "rda_internal.h"
@@ -36,11 +36,13 @@ constexpr int kThreads = 256;
 // Row r of a tile keeps 16-byte granule j at j ^ swizzle(r): sixteen
 // consecutive rows read at one granule (Kn, Kp) and four consecutive rows
 // read at four adjacent granules (V, transposing) fall on distinct banks.
+template <int kBufs>
 struct Lds {
-    uint16_t Kn[2][kBN * kMlaNope];   // 16 granules a row, j ^ (r & 15)
-    uint16_t Kp[2][kBN * kMlaPe];     // 8 granules a row, j ^ ((r >> 1) & 7)
-    uint16_t V[2][kBN * kMlaV];       // 16 granules a row, j ^ ((r & 3) << 2)
+    uint16_t Kn[kBufs][kBN * kMlaNope];   // 16 granules a row, j ^ (r & 15)
+    uint16_t Kp[kBufs][kBN * kMlaPe];     // 8 granules a row, j ^ ((r >> 1) & 7)
+    uint16_t V[kBufs][kBN * kMlaV];       // 16 granules a row, j ^ ((r & 3) << 2)
 };
+constexpr int kDma = 10;   // transfers of a wave per tile
 
 struct Dma {
     const MlaPrefillArgs& A;
@@ -50,7 +52,8 @@ struct Dma {
 
     // This wave's 10 KiB of the tile at key k0: 4 + 4 + 2 KiB of Kn, V, Kp.
     // Rows behind the last key repeat it.
-    __device__ __forceinline__ void issue(int k0, Lds& t, int buf) const {
+    template <int kBufs>
+    __device__ __forceinline__ void issue(int k0, Lds<kBufs>& t, int buf) const {
         const int last = lk - 1 - k0;
         const uint16_t* kt = kv + int64_t(k0) * A.kv_stride;
         const uint16_t* pt = pe + int64_t(k0) * A.pe_stride;
@@ -76,7 +79,8 @@ struct Dma {
 // the second 32 keys and the 16-key steps are constant offsets from them.
 struct Addr {
     uint32_t kn[8], kp[4], v[4];
-    __device__ __forceinline__ Addr(const Lds& t, int l) {
+    template <int kBufs>
+    __device__ __forceinline__ Addr(const Lds<kBufs>& t, int l) {
         const int r = l & 31, g = l >> 5, j = l & 15;
 #pragma unroll
         for (int m = 0; m < 8; ++m) kn[m] = lds_addr(t.Kn) + r * 256 + 16 * ((2 * m + g) ^ (r & 15));
@@ -142,8 +146,9 @@ __device__ __forceinline__ void add_masked_values(const MlaPrefillArgs& A, const
     }
 }
 
-__global__ __launch_bounds__(kThreads, 2) void mla_prefill_kernel(const MlaPrefillArgs A) {
-    __shared__ __attribute__((aligned(256))) Lds lds;
+template <int kBufs>
+__global__ __launch_bounds__(kThreads, 4 / kBufs) void mla_prefill_kernel(const MlaPrefillArgs A) {
+    __shared__ __attribute__((aligned(256))) Lds<kBufs> lds;
     const int w = wave_id(), l = threadIdx.x & 63, g = l >> 5;
     // the latest queries (of a causal prompt: those with the most keys) of all
     // heads first, so that the last to start are short (head by head instead:
@@ -186,12 +191,10 @@ __global__ __launch_bounds__(kThreads, 2) void mla_prefill_kernel(const MlaPrefi
     auto step = [&](auto buf_c, int n) {
         constexpr int kBuf = decltype(buf_c)::value;
         const int k0 = n * kBN;
-        if (n + 1 < ntiles) {
-            dma.issue(k0 + kBN, lds, kBuf ^ 1);
-            wait_vm<10>();
-        } else {
-            wait_vm<0>();
-        }
+        // tile n + kBufs - 1 goes where n - 1 was (behind the last tile it comes
+        // again, so that the number of transfers in flight is always the same)
+        dma.issue(min(n + kBufs - 1, ntiles - 1) * kBN, lds, (kBuf + kBufs - 1) % kBufs);
+        wait_vm<kDma*(kBufs - 1)>();
         raw_barrier();
         if (k0 < any_see) {
             f32x16 s[2] = {};
@@ -250,11 +253,19 @@ __global__ __launch_bounds__(kThreads, 2) void mla_prefill_kernel(const MlaPrefi
         }
         raw_barrier();
     };
-    if (ntiles > 0) dma.issue(0, lds, 0);
-    for (int n = 0; n < ntiles; n += 2) {
+    if (ntiles > 0) {
+#pragma unroll
+        for (int d = 0; d < kBufs - 1; ++d) dma.issue(min(d, ntiles - 1) * kBN, lds, d);
+    }
+    for (int n = 0; n < ntiles; n += kBufs) {
         step(std::integral_constant<int, 0>{}, n);
         if (n + 1 < ntiles) step(std::integral_constant<int, 1>{}, n + 1);
+        if constexpr (kBufs == 4) {
+            if (n + 2 < ntiles) step(std::integral_constant<int, 2>{}, n + 2);
+            if (n + 3 < ntiles) step(std::integral_constant<int, 3>{}, n + 3);
+        }
     }
+    wait_vm<0>();   // nothing may land in memory that is another workgroup's
     if (qi >= S.lq) return;
     if (left_from >= 0)
         add_masked_values(A, dma.kv, dma.pe, qrow, left_from, limit, c, mu, g, acc);
@@ -302,7 +313,12 @@ hipError_t launch_mla_prefill(const MlaPrefillArgs& A, hipStream_t stream) {
         W.slots = int32_t(wide);
         return launch_mla_prefill_wide(W, stream);
     }
-    mla_prefill_kernel<<<dim3(unsigned(A.slots * A.heads)), dim3(kThreads), 0, stream>>>(A);
+    // four tiles' memory where every workgroup has a CU for itself: 512 queries
+    // over 8704 keys x 32 heads 271 us for 323, 2048 x 8 70 for 77, 30 over 1959
+    // x 16 64 for 72; two tiles' memory and two workgroups a CU otherwise
+    const dim3 grid(unsigned(A.slots * A.heads));
+    if (A.slots * A.heads <= kMlaWorkgroups) mla_prefill_kernel<4><<<grid, dim3(kThreads), 0, stream>>>(A);
+    else mla_prefill_kernel<2><<<grid, dim3(kThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
