@@ -7,10 +7,11 @@
 //
 // One workgroup of four waves takes 128 queries of one head, a wave 32 of
 // them, and walks the keys in tiles of 64 that arrive by LDS-DMA one tile
-// ahead (three where a workgroup has a CU for itself).  The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that
-// a lane owns one query: the D registers of S^T are, rounded to bf16, the B
-// operand of the second product in the order (4g .. 4g+3, 8 + 4g ..) of the
-// keys, which the transposing reads of V follow.  P never leaves registers.
+// ahead (three where a workgroup has a CU for itself).  The products are
+// transposed, S^T = K Q^T and O^T = V^T P^T, so that a lane owns one query: the
+// D registers of S^T are, rounded to bf16, the B operand of the second product
+// in the order (4g .. 4g+3, 8 + 4g ..) of the keys, which the transposing reads
+// of V follow.  P never leaves registers.
 //
 // Two workgroups share a CU's LDS (two tiles of 40 KiB each), so one's products
 // run beside the other's exponentials.  An operand read from LDS feeds one

@@ -13,8 +13,8 @@
 // in slices of two products that are written out in that order.  Keys and
 // values of a step arrive by LDS-DMA, six steps' memory in turn.
 //
-// Measured: 8192 causal tokens of 32 heads 858 us, 801 TFLOP/s of the causal
-// half; 4096 x 16 over all keys 182 us, 945; 16384 x 32 2692 us, 1021.  A step
+// Measured: 8192 causal tokens of 32 heads 858 us called back to back, 801
+// TFLOP/s of the causal half (728 us, 944, between other work); 4096 x 16 over all keys 182 us, 945; 16384 x 32 2692 us, 1021.  A step
 // takes about 2600 cycles of which its 40 products are 1280; issue slots are
 // half used and about a third of the time goes to waits on LDS.  The clock
 // counts too: the same calls on zeros (less switching, higher clock) take 711
