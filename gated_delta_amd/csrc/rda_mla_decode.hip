@@ -745,13 +745,13 @@ __global__ __launch_bounds__(kThreads) void mla_combine_kernel(const MlaDecodeAr
         sum[1] *= f;
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-            const float w = i0 + e >= n || ml[e][0] == -INFINITY
-                ? 0.f : __builtin_amdgcn_exp2f(ml[e][0] - most);
-            if (w != 0.f) {   // (a piece without keys has no sums to speak of)
-                total = fmaf(ml[e][1], w, total);
-                sum[0] += x[e][0] * w;
-                sum[1] += x[e][1] * w;
-            }
+            if (i0 + e >= n) break;
+            // (every piece counts: one whose scores are all NaN has the maximum
+            // -inf like one without keys, but NaN for its sums)
+            const float w = ml[e][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[e][0] - most);
+            total = fmaf(ml[e][1], w, total);
+            sum[0] += x[e][0] * w;
+            sum[1] += x[e][1] * w;
         }
     }
     const float inv = inverse(total);
