@@ -34,12 +34,12 @@ constexpr int kThreads = 256;
 struct Choice {
     int accepted;         // drafts accepted
     bool refused;         // one was refused
-    int drafted;          // that token, or -1
+    int drafted;          // that token, -1 where it is outside the vocabulary
     const float* p;       // target row
     const float* q;       // draft row or nullptr
 };
 
-constexpr int kNoneRefused = INT_MIN;
+constexpr int kNoneRefused = INT_MIN;   // in the workspace, in a refused token's place
 typedef double f64x2 __attribute__((ext_vector_type(2)));
 
 // The rows of probabilities that the choice leads to.
@@ -58,7 +58,9 @@ __device__ __forceinline__ Choice choose(const VerifyArgs& A, int b) {
     int d = -1;
     if (l < count) {
         d = A.tokens[int64_t(b) * D + l];
-        if (d >= 0 && d < A.vocab) {
+        if (d < 0 || d >= A.vocab) {
+            d = -1;   // refused, whatever it is: no value of the caller's is kept as a mark
+        } else {
             const float p = A.target[(int64_t(b) * (D + 1) + l) * A.target_stride + d];
             const float q = A.draft ? A.draft[(int64_t(b) * D + l) * A.draft_stride + d] : 1.f;
             ok = double(A.uniforms[int64_t(b) * (D + 1) + l]) * double(q) < double(p);
