@@ -75,11 +75,11 @@ __device__ __forceinline__ Choice choose(const VerifyArgs& A, int b) {
     return c;
 }
 
-// The weight of token j (`point`: nothing for the refused token); what is not a positive
-// finite number weighs nothing.
+// The weight of token j (`point`: nothing for the refused token); nothing where it or the
+// target's probability is not a positive finite number.
 __device__ __forceinline__ double weight(const Choice& c, bool point, int j, float p, float q) {
     double w = double(p) - double(q);
-    if (point && j == c.drafted) w = 0.0;
+    if (!(p > 0.f) || (point && j == c.drafted)) w = 0.0;
     return w > 0.0 && w < double(INFINITY) ? w : 0.0;
 }
 

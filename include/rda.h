@@ -617,8 +617,8 @@ size_t rda_verify_drafts_workspace_bytes(int32_t batch, int32_t vocab);
  *
  *   target        [batch, drafts + 1] rows target_stride values apart of
  *                 `vocab` fp32 probabilities: after the current token and
- *                 after each draft.  They need not sum to 1; what is not a
- *                 positive finite number weighs nothing
+ *                 after each draft.  They need not sum to 1; a token weighs
+ *                 nothing where p_r or w is not a positive finite number
  *   draft         [batch, drafts] rows draft_stride values apart of the
  *                 probabilities the drafts were drawn from, or NULL for
  *                 drafts without any (q_i = 1 at d_i and 0 elsewhere)

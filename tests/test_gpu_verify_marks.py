@@ -36,3 +36,16 @@ def test_smallest_token_among_others(dev, V):
     tok[::2, 1] = INT_MIN
     run(dev, target, draft, tok, u, num)
     run(dev, target, None, tok, u, num)
+
+
+@pytest.mark.parametrize("p0", [-1.0, 0.0, float("nan"), float("-inf"), float("inf")])
+@pytest.mark.parametrize("q0", [-2.0, float("-inf"), 0.0])
+def test_a_target_that_is_not_positive_and_finite_weighs_nothing(dev, p0, q0):
+    """Whatever the draft row holds there: p = (p0, 1/2, 1/2), q = (q0, 0, 1/4)
+    leave (0, 1/2, 1/4)."""
+    p = torch.tensor([p0, 0.5, 0.5]).repeat(4, 2, 1).to(dev)
+    q = torch.tensor([q0, 0.0, 0.25]).repeat(4, 1, 1).to(dev)
+    u = torch.tensor([[0.0, 0.0], [0.0, 0.6], [0.0, 0.7], [0.0, 0.99]], device=dev)
+    tok = torch.full((4, 1), -1, dtype=torch.int32, device=dev)
+    acc, out = rda.rda_verify_drafts(p, q, tok, u)
+    assert acc.tolist() == [1] * 4 and out[:, 0].tolist() == [1, 1, 2, 2]
