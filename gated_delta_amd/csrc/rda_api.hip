@@ -1140,6 +1140,8 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
                           float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (rda_status st = check_mla_decode_sizes(batch, tokens, num_heads, prefix_len); st != RDA_OK)
         return st;
+    // the combine kernel: four query rows a workgroup
+    if ((int64_t(batch) * tokens * num_heads + 3) / 4 >= kMaxWorkgroups) return RDA_ERR_SHAPE;
     if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
         return st;
     if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;

@@ -558,7 +558,9 @@ size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num
  *               bounds (an id outside [0, num_pages) reads some page)
  *   prefix_table  device int32 [ceil(prefix_len / page_tokens)], not read
  *               where prefix_len = 0
- *   tokens in [0, RDA_DECODE_MAX_TOKENS]; scale finite and > 0
+ *   tokens in [0, RDA_DECODE_MAX_TOKENS]; scale finite and > 0; tokens x H
+ *               at most 2^24, batch x tokens x H at most 2^26 - 4
+ *               (RDA_ERR_SHAPE)
  *   o           [batch, tokens, H, 512] bf16; lse [batch, tokens, H] fp32 or
  *               NULL
  * The lengths are read on the device: a captured call may be replayed with
