@@ -1145,7 +1145,9 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
     if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
         return st;
     if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
-    if (int64_t(table_width) * page_tokens > INT32_MAX ||
+    // row numbers are 32 bits in the kernel, those of the tiles that it fetches
+    // (as zeros) behind the last too: up to nine tiles of 32
+    if (int64_t(table_width) * page_tokens > (int64_t(1) << 31) - 1024 ||
         !mla_tiles_ok((int64_t(tokens) * num_heads + 31) / 32 * 32 * batch,
                       int64_t(table_width) * page_tokens))
         return RDA_ERR_SHAPE;

@@ -551,7 +551,7 @@ size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num
  *               RDA_MLA_MAX_PAGE] (RDA_ERR_UNSUPPORTED)
  *   block_table device int32 [batch, table_width]: the pages of a sequence's
  *               rows in order; entries behind its last page are not read
- *               (table_width x page_tokens below 2^31, and batch x tokens x H / 32
+ *               (table_width x page_tokens at most 2^31 - 1024, and batch x tokens x H / 32
  *               x that / 32 too, as with prefix_len: RDA_ERR_SHAPE)
  *   kv_lens     device int32 [batch]; clamped to [0, table_width x
  *               page_tokens].  Page ids are trusted, but never used out of
