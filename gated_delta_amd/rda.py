@@ -3,12 +3,14 @@
 Every function here has the name of the C entry point it calls (see
 ``include/rda.h``) and does no arithmetic of its own: it checks tensor
 dtypes, devices and shapes, allocates outputs and the workspace with
-``torch.empty`` on the caller's device, validates ``cu_seqlens`` on a host
-copy, and passes raw device pointers plus the current HIP stream.  If the
+``torch.empty`` on the caller's device (from the pool of the stream that is
+launched on), validates ``cu_seqlens`` on a host copy, and passes raw device
+pointers plus the given or the current HIP stream.  If the
 library is not built, the first call raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -185,6 +187,37 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _pool(stream):
+    """The memory that a call makes for itself comes from the pool of the stream
+    it is launched on.  A block of the current stream's pool may still be in use
+    by earlier work there, which ``stream`` does not wait for, and a temporary
+    given back to that pool could be overwritten before ``stream`` has read it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """An output for the caller: also kept from reuse until the caller's
+    current stream is past what it had queued when it let go of it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with _pool(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _scratch(need: int, dev, stream) -> torch.Tensor:
+    """Workspace for one call."""
+    with _pool(stream):
+        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+
+
+def _upload(x: np.ndarray, dev, stream) -> torch.Tensor:
+    """A host array on the device, for one call."""
+    with _pool(stream):
+        return torch.from_numpy(x).to(dev)
 
 
 def check_cu_seqlens(cu, total_tokens: int) -> np.ndarray:
@@ -453,6 +486,8 @@ def _stream_on(dev: torch.device, stream) -> int:
         if _raw_stream is not None:
             return _raw_stream(dev.index)
         stream = torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream must be on {dev}, got {stream.device}")
     return stream.cuda_stream
 
 
@@ -480,7 +515,7 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     return stride[0] if shape[0] > 1 else width
 
 
-def _offsets(cu, name: str, total: int, device) -> Optional[torch.Tensor]:
+def _offsets(cu, name: str, total: int, device, stream) -> Optional[torch.Tensor]:
     """Packed offsets on the device: a device int32 tensor as it is (trusted,
     like the C entry points do; no copy to the host), anything else checked
     on the host first."""
@@ -491,7 +526,7 @@ def _offsets(cu, name: str, total: int, device) -> Optional[torch.Tensor]:
         if cu.dim() != 1 or cu.numel() < 2:
             raise ValueError(f"{name} must be 1-D with at least 2 entries")
         return cu
-    return torch.from_numpy(check_cu_seqlens(cu, total)).to(device)
+    return _upload(check_cu_seqlens(cu, total), device, stream)
 
 
 def rda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float,
@@ -517,14 +552,14 @@ def rda_mla_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale
     qs = _need_rows(q, "q", torch.bfloat16, (Tq, H, RDA_MLA_QK), dev)
     ks = _need_rows(kv, "kv", torch.bfloat16, (Tk, H, RDA_MLA_KV), dev)
     ps = _need_rows(k_pe, "k_pe", torch.bfloat16, (Tk, RDA_MLA_PE), dev)
-    cq, ck = _offsets(cu_q, "cu_q", Tq, dev), _offsets(cu_k, "cu_k", Tk, dev)
+    cq, ck = _offsets(cu_q, "cu_q", Tq, dev, stream), _offsets(cu_k, "cu_k", Tk, dev, stream)
     if ck is not None and (cq is None or ck.numel() != cq.numel()):
         raise ValueError("cu_k needs a cu_q of as many entries")
     if o is None:
-        o = torch.empty((Tq, H, RDA_MLA_V), dtype=torch.bfloat16, device=dev)
+        o = _empty((Tq, H, RDA_MLA_V), torch.bfloat16, dev, stream)
     _need(o, "o", torch.bfloat16, (Tq, H, RDA_MLA_V), dev)
     if lse is None and want_lse:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+        lse = _empty((Tq, H), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, (Tq, H), dev)
     with _On(dev):
@@ -584,15 +619,14 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
         if prefix_table.numel() * cache.shape[1] < prefix_len:
             raise ValueError("prefix_table holds fewer rows than prefix_len")
     if o is None:
-        o = torch.empty((B, T, H, RDA_MLA_LATENT), dtype=torch.bfloat16, device=dev)
+        o = _empty((B, T, H, RDA_MLA_LATENT), torch.bfloat16, dev, stream)
     _need(o, "o", torch.bfloat16, (B, T, H, RDA_MLA_LATENT), dev)
     if lse is None and want_lse:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = _empty((B, T, H), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, H), dev)
     if workspace is None:
-        workspace = _workspace(rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)),
-                               dev, stream)
+        workspace = _scratch(rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)), dev, stream)
     with _On(dev):
         st = lib_.rda_mla_decode(_addr(q), _addr(cache), page_stride, cache.shape[0], cache.shape[1],
                                  _addr(block_table), block_table.shape[1], _addr(kv_lens),
@@ -603,14 +637,6 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
     if st != 0:
         raise RdaError(st, "rda_mla_decode")
     return o, lse
-
-
-def _workspace(need: int, dev, stream) -> torch.Tensor:
-    """Scratch for one call, kept from reuse until the call's stream is past it."""
-    w = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        w.record_stream(stream)
-    return w
 
 
 def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -637,7 +663,7 @@ def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     N = block_table.shape[0]
     _need(block_table, "block_table", torch.int32, (N, block_table.shape[1]), dev)
     _need(kv_lens, "kv_lens", torch.int32, (N,), dev)
-    cu = _offsets(cu_seqlens, "cu_seqlens", T, dev)
+    cu = _offsets(cu_seqlens, "cu_seqlens", T, dev, stream)
     if cu is not None and cu.numel() != N + 1:
         raise ValueError("cu_seqlens must have one entry more than block_table has rows")
     if weight is not None:
@@ -699,13 +725,13 @@ def rda_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     if num_drafts is not None:
         _need(num_drafts, "num_drafts", torch.int32, (B,), dev)
     if accept is None:
-        accept = torch.empty((B,), dtype=torch.int32, device=dev)
+        accept = _empty((B,), torch.int32, dev, stream)
     _need(accept, "accept", torch.int32, (B,), dev)
     if out_tokens is None:
-        out_tokens = torch.empty((B, T), dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, T), torch.int32, dev, stream)
     _need(out_tokens, "out_tokens", torch.int32, (B, T), dev)
     if workspace is None:
-        workspace = _workspace(rda_verify_drafts_workspace_bytes(B, V), dev, stream)
+        workspace = _scratch(rda_verify_drafts_workspace_bytes(B, V), dev, stream)
     with _On(dev):
         st = lib_.rda_verify_drafts(_addr(target), ts, _addr(draft) if T > 1 else None, ds,
                                     _addr(draft_tokens), _addr(uniforms), _addr(num_drafts), B, T - 1,
