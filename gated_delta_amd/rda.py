@@ -278,21 +278,21 @@ def rda_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: torch.Tens
                 and cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous():
             cu_dev = cu_seqlens
         else:
-            cu_dev = torch.from_numpy(cu_host).to(dev)
+            cu_dev = _upload(cu_host, dev, stream)
     else:
         N, cu_dev = 1, None
     if S0 is not None:
         _need(S0, "S0", torch.float32, (N, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=torch.float32, device=dev)
+        o = _empty((T, H, dv), torch.float32, dev, stream)
     _need(o, "o", torch.float32, (T, H, dv), dev)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        S_final = _empty((N, H, dv, dk), torch.float32, dev, stream)
     if S_final is not None:
         _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_workspace_bytes(N, T, H, dk, dv)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(need, dev, stream)
     args = [_ptr(q), _ptr(k), _ptr(v), dt, _ptr(a), _ptr(b), _ptr(cu_dev), N, T, H, dk, dv,
             _ptr(S0), _ptr(o), _ptr(S_final), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream_handle(stream)]
@@ -371,7 +371,7 @@ def rda_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: torch.
     _need(b, "b", torch.float32, (B, H), dev)
     _need(S, "S", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=torch.float32, device=dev)
+        o = _empty((B, H, dv), torch.float32, dev, stream)
     _need(o, "o", torch.float32, (B, H, dv), dev)
     st = lib_.rda_decode_step(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(a), _ptr(b), B, H, dk, dv,
                               _ptr(S), _ptr(o), _stream_handle(stream))
@@ -410,7 +410,7 @@ def _decode_tokens(name, q, k, v, a, b, S_in, S_out, accept, o, stream, diag):
         _need(accept, "accept", torch.int32, (B,), dev)
     if want_o:
         if o is None:
-            o = torch.empty((B, T, H, dv), dtype=torch.float32, device=dev)
+            o = _empty((B, T, H, dv), torch.float32, dev, stream)
         _need(o, "o", torch.float32, (B, T, H, dv), dev)
     else:
         o = None
@@ -755,9 +755,9 @@ def rda_chunk_table(cu_seqlens, num_seqs: int, total_tokens: int, device="cuda",
     mc = rda_max_chunks(num_seqs, total_tokens)
     if mc < 0:
         raise ValueError("bad sizes")
-    rec = torch.empty((max(mc, 1), 4), dtype=torch.int32, device=device)
-    seq_off = torch.empty((num_seqs + 1,), dtype=torch.int32, device=device)
-    nch = torch.empty((1,), dtype=torch.int32, device=device)
+    rec = _empty((max(mc, 1), 4), torch.int32, device, stream)
+    seq_off = _empty((num_seqs + 1,), torch.int32, device, stream)
+    nch = _empty((1,), torch.int32, device, stream)
     st = lib_.rda_chunk_table(_ptr(cu_seqlens), int(num_seqs), int(total_tokens), _ptr(rec),
                               _ptr(seq_off), _ptr(nch), _stream_handle(stream))
     if st != 0:
@@ -800,7 +800,7 @@ def rda_output_norm_gate(o: torch.Tensor, g: Optional[torch.Tensor], *,
     if o_dt is None:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _empty(shape, out_dtype, dev, stream)
     _need(out, "out", out_dtype, shape, dev)
     st = lib_.rda_output_norm_gate(_ptr(o), _ptr(g), g_dt, _ptr(weight), float(eps),
                                    _GATE_ACTS[act], rows, dv, _ptr(out), o_dt,
@@ -844,7 +844,7 @@ def rda_prefill_norm_gate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: 
     if cu_seqlens is not None:
         cu_host = check_cu_seqlens(cu_seqlens, T)
         N = cu_host.shape[0] - 1
-        cu_dev = torch.from_numpy(cu_host).to(dev)
+        cu_dev = _upload(cu_host, dev, stream)
     else:
         N, cu_dev = 1, None
     if S0 is not None:
@@ -865,15 +865,15 @@ def rda_prefill_norm_gate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: 
     if o_dt is None:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     if out is None:
-        out = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
+        out = _empty((T, H, dv), out_dtype, dev, stream)
     _need(out, "out", out_dtype, (T, H, dv), dev)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        S_final = _empty((N, H, dv, dk), torch.float32, dev, stream)
     if S_final is not None:
         _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_norm_gate_workspace_bytes(N, T, H, dk, dv)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(need, dev, stream)
     st = lib_.rda_prefill_norm_gate(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(a), _ptr(b),
                                     _ptr(cu_dev), N, T, H, dk, dv, _ptr(S0), _ptr(g), g_dt,
                                     _ptr(weight), float(eps), _GATE_ACTS[act], _ptr(out), o_dt,
@@ -925,15 +925,15 @@ def rda_prologue(x_q: torch.Tensor, x_k: torch.Tensor, x_v: torch.Tensor,
     if cu_seqlens is not None:
         cu_np = check_cu_seqlens(cu_seqlens, T)
         num_seqs = len(cu_np) - 1
-        cu_dev = torch.from_numpy(cu_np).to(dev)
+        cu_dev = _upload(cu_np, dev, stream)
     hshape = (num_seqs, 3, max(K - 1, 0), H, d)
     for name, t in (("hist_in", hist_in), ("hist_out", hist_out)):
         if t is not None:
             _need(t, name, torch.bfloat16, hshape, dev)
     if conv_act not in _CONV_ACTS:
         raise ValueError(f"conv_act must be one of {sorted(_CONV_ACTS)}")
-    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(3))
-    a, b = (torch.empty(lead + (H,), dtype=torch.float32, device=dev) for _ in range(2))
+    q, k, v = (_empty(shape, torch.bfloat16, dev, stream) for _ in range(3))
+    a, b = (_empty(lead + (H,), torch.float32, dev, stream) for _ in range(2))
     st = lib_.rda_prologue(_ptr(x_q), _ptr(x_k), _ptr(x_v), RDA_BF16, _ptr(conv_w), K,
                            _CONV_ACTS[conv_act], _ptr(hist_in), _ptr(hist_out), _ptr(beta_raw),
                            _ptr(delta), _ptr(g_log), float(decay_floor), float(l2_eps),
@@ -979,7 +979,7 @@ def rda_decode_step_prologue(x_q: torch.Tensor, x_k: torch.Tensor, x_v: torch.Te
     if conv_act not in _CONV_ACTS:
         raise ValueError(f"conv_act must be one of {sorted(_CONV_ACTS)}")
     if o is None:
-        o = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+        o = _empty((B, H, d), torch.float32, dev, stream)
     _need(o, "o", torch.float32, (B, H, d), dev)
     st = lib_.rda_decode_step_prologue(_ptr(x_q), _ptr(x_k), _ptr(x_v), RDA_BF16, _ptr(conv_w),
                                        K, _CONV_ACTS[conv_act], _ptr(hist_in), _ptr(hist_out),
@@ -1020,18 +1020,18 @@ def rda_prefill_diag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
     if cu_seqlens is not None:
         cu_np = check_cu_seqlens(cu_seqlens, T)
         N = len(cu_np) - 1
-        cu_dev = torch.from_numpy(cu_np).to(dev)
+        cu_dev = _upload(cu_np, dev, stream)
     if S0 is not None:
         _need(S0, "S0", torch.float32, (N, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=torch.float32, device=dev)
+        o = _empty((T, H, dv), torch.float32, dev, stream)
     _need(o, "o", torch.float32, (T, H, dv), dev)
     if S_final is None:
-        S_final = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        S_final = _empty((N, H, dv, dk), torch.float32, dev, stream)
     _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_diag_workspace_bytes(N, T, H, dk, dv)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(need, dev, stream)
     st = lib_.rda_prefill_diag(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), _ptr(b),
                                _ptr(cu_dev), N, T, H, dk, dv, _ptr(S0), _ptr(o), _ptr(S_final),
                                _ptr(workspace), workspace.numel(), _stream_handle(stream))
@@ -1058,7 +1058,7 @@ def rda_decode_step_diag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alph
     _need(b, "b", torch.float32, (B, H), dev)
     _need(S, "S", torch.float32, (B, H, dv, dk), dev)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=torch.float32, device=dev)
+        o = _empty((B, H, dv), torch.float32, dev, stream)
     _need(o, "o", torch.float32, (B, H, dv), dev)
     st = lib_.rda_decode_step_diag(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), _ptr(b), B, H,
                                    dk, dv, _ptr(S), _ptr(o), _stream_handle(stream))

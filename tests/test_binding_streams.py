@@ -107,6 +107,34 @@ CALLS = {
 MADE = {"mla_prefill": 4, "mla_decode": 3, "mla_append": 1, "verify_drafts": 3}
 
 
+def mixer(*lead):
+    """q, k, v, a, b of the mixer."""
+    return [bf(*lead, 128) for _ in range(3)] + [f32(*lead), f32(*lead)]
+
+
+def diag(*lead):
+    return [bf(*lead, 128) for _ in range(3)] + [f32(*lead, 128), f32(*lead)]
+
+
+RAW = [bf(4, 2, 128) for _ in range(3)] + [f32(3, 2, 128, 4), f32(4, 2), f32(4, 2)]
+CU = [0, 1, 6]
+CALLS.update({
+    "prefill": lambda s: rda.rda_prefill(*mixer(6, 2), CU, stream=s),
+    "prefill_norm_gate": lambda s: rda.rda_prefill_norm_gate(*mixer(6, 2), bf(6, 2, 128), CU, stream=s),
+    "prefill_diag": lambda s: rda.rda_prefill_diag(*diag(6, 2), cu_seqlens=CU, stream=s),
+    "decode_step": lambda s: rda.rda_decode_step(*mixer(3, 2), f32(3, 2, 128, 128), stream=s),
+    "decode_step_diag": lambda s: rda.rda_decode_step_diag(*diag(3, 2), f32(3, 2, 128, 128), stream=s),
+    "decode_tokens": lambda s: rda.rda_decode_tokens(*mixer(3, 4, 2), f32(3, 2, 128, 128), stream=s),
+    "decode_tokens_diag": lambda s: rda.rda_decode_tokens_diag(*diag(3, 4, 2), f32(3, 2, 128, 128), stream=s),
+    "output_norm_gate": lambda s: rda.rda_output_norm_gate(f32(5, 128), bf(5, 128), stream=s),
+    "prologue": lambda s: rda.rda_prologue(*RAW, cu_seqlens=[0, 3, 4], stream=s),
+    "decode_step_prologue": lambda s: rda.rda_decode_step_prologue(*RAW, f32(4, 2, 128, 128), stream=s),
+    "chunk_table": lambda s: rda.rda_chunk_table(ints(*CU), 2, 6, device=DEV, stream=s),
+})
+MADE.update(prefill=4, prefill_norm_gate=4, prefill_diag=4, decode_step=1, decode_step_diag=1, decode_tokens=1,
+            decode_tokens_diag=1, output_norm_gate=1, prologue=6, decode_step_prologue=1, chunk_table=3)
+
+
 @pytest.mark.parametrize("name", CALLS)
 def test_memory_of_the_launch_stream(fake, name):
     s = FakeStream("side")
