@@ -208,10 +208,19 @@ def _empty(shape, dtype, dev, stream) -> torch.Tensor:
     return t
 
 
-def _scratch(need: int, dev, stream) -> torch.Tensor:
-    """Workspace for one call."""
-    with _pool(stream):
-        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev, stream) -> torch.Tensor:
+    """The caller's workspace (its size is the library's to check), or one for
+    this call."""
+    if workspace is None:
+        with _pool(stream):
+            return torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
 
 
 def _upload(x: np.ndarray, dev, stream) -> torch.Tensor:
@@ -291,8 +300,7 @@ def rda_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: torch.Tens
     if S_final is not None:
         _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_workspace_bytes(N, T, H, dk, dv)
-    if workspace is None:
-        workspace = _scratch(need, dev, stream)
+    workspace = _scratch(workspace, need, dev, stream)
     args = [_ptr(q), _ptr(k), _ptr(v), dt, _ptr(a), _ptr(b), _ptr(cu_dev), N, T, H, dk, dv,
             _ptr(S0), _ptr(o), _ptr(S_final), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream_handle(stream)]
@@ -625,8 +633,7 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
         lse = _empty((B, T, H), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, H), dev)
-    if workspace is None:
-        workspace = _scratch(rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)), dev, stream)
+    workspace = _scratch(workspace, rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)), dev, stream)
     with _On(dev):
         st = lib_.rda_mla_decode(_addr(q), _addr(cache), page_stride, cache.shape[0], cache.shape[1],
                                  _addr(block_table), block_table.shape[1], _addr(kv_lens),
@@ -730,8 +737,7 @@ def rda_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     if out_tokens is None:
         out_tokens = _empty((B, T), torch.int32, dev, stream)
     _need(out_tokens, "out_tokens", torch.int32, (B, T), dev)
-    if workspace is None:
-        workspace = _scratch(rda_verify_drafts_workspace_bytes(B, V), dev, stream)
+    workspace = _scratch(workspace, rda_verify_drafts_workspace_bytes(B, V), dev, stream)
     with _On(dev):
         st = lib_.rda_verify_drafts(_addr(target), ts, _addr(draft) if T > 1 else None, ds,
                                     _addr(draft_tokens), _addr(uniforms), _addr(num_drafts), B, T - 1,
@@ -872,8 +878,7 @@ def rda_prefill_norm_gate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: 
     if S_final is not None:
         _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_norm_gate_workspace_bytes(N, T, H, dk, dv)
-    if workspace is None:
-        workspace = _scratch(need, dev, stream)
+    workspace = _scratch(workspace, need, dev, stream)
     st = lib_.rda_prefill_norm_gate(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(a), _ptr(b),
                                     _ptr(cu_dev), N, T, H, dk, dv, _ptr(S0), _ptr(g), g_dt,
                                     _ptr(weight), float(eps), _GATE_ACTS[act], _ptr(out), o_dt,
@@ -1030,8 +1035,7 @@ def rda_prefill_diag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
         S_final = _empty((N, H, dv, dk), torch.float32, dev, stream)
     _need(S_final, "S_final", torch.float32, (N, H, dv, dk), dev)
     need = rda_prefill_diag_workspace_bytes(N, T, H, dk, dv)
-    if workspace is None:
-        workspace = _scratch(need, dev, stream)
+    workspace = _scratch(workspace, need, dev, stream)
     st = lib_.rda_prefill_diag(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), _ptr(b),
                                _ptr(cu_dev), N, T, H, dk, dv, _ptr(S0), _ptr(o), _ptr(S_final),
                                _ptr(workspace), workspace.numel(), _stream_handle(stream))
