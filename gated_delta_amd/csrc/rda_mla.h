@@ -70,8 +70,9 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16& s) {
 // compiler wait for every transfer in flight before any LDS read (it cannot
 // tell the buffers apart), which would end the prefetch; here the waits are
 // the caller's (wait_vm and a barrier before the first read).  It writes M0,
-// which nothing else in these kernels uses.  kOnce: for memory that is read
-// once (a non-temporal load).
+// which cannot be named as changed (the compiler reserves it) and which nothing
+// else in these kernels uses (tests/test_accumulators.py looks).  kOnce: for
+// memory that is read once (a non-temporal load).
 template <bool kOnce = false>
 __device__ __forceinline__ void dma16_at(const void* base, uint32_t off, uint32_t lds) {
     if constexpr (kOnce)

@@ -12,10 +12,12 @@ namespace rda {
 // statements below only.  The compiler is not told that they hold values (left
 // to it, sums that fill much of that file are copied to memory and back around
 // every branch), but that every statement may change them, so it keeps nothing
-// of its own there; the scores' products, which it would place there too, have
-// ordinary registers.  It does not see matrix products in here either: each waits the
-// two states that ordinary arithmetic needs before one reads its result
-// (s_nop 1), and settle / scores_done stand before a result is read.
+// of its own there across one.  Between two it could: tests/test_accumulators.py
+// looks through the assembly that it does not.  The scores' products, which it
+// would place there too, have ordinary registers.  It does not see matrix
+// products in here either: each waits the two states that ordinary arithmetic
+// needs before one reads its result (s_nop 1), and settle / scores_done stand
+// before a result is read.
 #define RDA_A10(t) "a" #t "0", "a" #t "1", "a" #t "2", "a" #t "3", "a" #t "4", "a" #t "5", \
                    "a" #t "6", "a" #t "7", "a" #t "8", "a" #t "9"
 #define RDA_ALL_ACC RDA_A10(), RDA_A10(1), RDA_A10(2), RDA_A10(3), RDA_A10(4), RDA_A10(5),    \
