@@ -113,6 +113,8 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
         const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
         const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
         A.prefix_per = int32_t(share > least ? share : least);
+        A.pre_bad = reinterpret_cast<int32_t*>(
+            take((size_t(A.prefix_units) + kMlaWorkgroups) * sizeof(int32_t)));
         const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_waves;
         A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));

@@ -355,7 +355,7 @@ struct MlaDecodeArgs {
     int32_t prefix_per;          // prefix tiles per workgroup
     // workspace
     int32_t* meta;               // per unit: first and last workgroup, or -1
-    int32_t* bad;                // per slot of partial sums
+    int32_t *bad, *pre_bad;      // per slot of partial sums
     float *part, *part_ml, *pre_part, *pre_ml;
 };
 hipError_t launch_mla_decode(const MlaDecodeArgs& A, hipStream_t stream);

@@ -215,7 +215,7 @@ struct Sink {
     int rows;          // query rows of the unit
     float* part;       // [unit rows][512]
     float* ml;         // [unit rows][2]
-    int32_t* bad;      // set where the last tiles held infinities or NaN (null: the prefix)
+    int32_t* bad;      // set where the last tiles held infinities or NaN
 };
 
 // Four channels of a row, and a row's statistics.
@@ -258,7 +258,7 @@ __device__ __forceinline__ void finish(const MlaDecodeArgs& A, Lds& lds, const S
     settle();
     raw_barrier();   // the tiles are read
     if (threadIdx.x == 0) {
-        if (sink.bad) *sink.bad = lds.bad;
+        *sink.bad = lds.bad;
         lds.bad = 0;
     }
     // each lane: its row's part of every key wave's sums, and the quotient
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_kernel(const MlaDecode
         sink.rows = min(32 * kRW, rows - unit * 32 * kRW);
         sink.part = A.pre_part + size_t(slot) * kMlaLatent * 32 * kRW;
         sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRW;
-        sink.bad = nullptr;   // (every query sees every row)
+        sink.bad = A.pre_bad + slot;
         piece<kRW, false>(A, lds, lane, Source{A.prefix_table, A.prefix_len}, first, last, sink);
         at += last - first;
     }
