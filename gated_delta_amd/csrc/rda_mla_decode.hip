@@ -30,8 +30,9 @@
 // 6.1; 32 sequences of 3 tokens 65 us (2.3 TB/s: 17 tiles a workgroup, about
 // 2 us each with 96 of 128 query rows in use, and 20 us to load queries and to
 // write and join sums); 12288 query rows (128 sequences of 3 tokens) behind 16384
-// shared rows: the prefix 455 us, 963 TFLOP/s.  One sequence of 777 rows takes 18 us, of
-// which the two kernels' launches and starts are most.
+// shared rows: the prefix 455 us, 963 TFLOP/s.  One sequence of 777 rows takes 19 us, 16
+// of them in this kernel for one tile a wave: the plan's sums over the lengths,
+// the first transfers and the exchange of query operands, one after the other.
 #include <type_traits>
 
 #include "rda_internal.h"

@@ -13,10 +13,15 @@
 // in the order (4g .. 4g+3, 8 + 4g ..) of the keys, which the transposing reads
 // of V follow.  P never leaves registers.
 //
+// The form with two tiles' memory does not fit its 256 registers: 20 go to
+// scratch, and where one comes back the compiler waits for every load in
+// flight, the transfers of the next tile among them.  Its prefetch is emptied
+// in every tile for that.
+//
 // Two workgroups share a CU's LDS (two tiles of 40 KiB each), so one's products
 // run beside the other's exponentials.  An operand read from LDS feeds one
-// product of 32 cycles, about as long as the CU's LDS needs for it, so LDS and
-// the matrix cores are equally busy.  Measured: 4096 new tokens of 5 sequences
+// product of 32 cycles, about as long as the CU's LDS needs for it, so neither
+// could be much less busy than the other.  Measured: 4096 new tokens of 5 sequences
 // behind 3001 cached ones, 16 heads, 115 us, 450 TFLOP/s; 2048 tokens of 32
 // heads 87 us; 65 tokens 13.9 us.  A few queries over a long context are the
 // weak side: a wave's tile after the other, 2 us each, most of it latency
@@ -185,8 +190,9 @@ __global__ __launch_bounds__(kThreads, 4 / kBufs) void mla_prefill_kernel(const 
     int left_from = -1;   // first key of the tiles left to add_masked_values
 
     const Addr addr(lds, l);
-    // the queries have arrived before the first transfer into LDS is issued:
-    // no wait of the compiler's own stands in the loop
+    // the queries have arrived before the first transfer into LDS is issued: no
+    // wait of the compiler's own for them stands in the loop (with two tiles'
+    // memory it has others, for registers that it keeps in scratch)
 #pragma unroll
     for (int mm = 0; mm < 12; ++mm) asm volatile("" : "+v"(qf[mm]));
     auto step = [&](auto buf_c, int n) {

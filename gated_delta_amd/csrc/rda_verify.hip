@@ -17,9 +17,10 @@
 // chunks so that a small batch fills the chip too; every workgroup derives r
 // itself, from a few scalars.  The pick kernel, one workgroup per sequence,
 // finds the chunk (each of its waves by itself, up to 64 chunks in one scan)
-// and reads only that again.  256 sequences of 259840 tokens: 85 us, 6.3 TB/s
-// for the 532 MB of the two rows each; 8 sequences of 32003: 17.9 us, the two
-// launches and a chain of small loads.
+// and reads only that again.  256 sequences of 259840 tokens: 85 us, 5.1
+// TB/s for the 437 MB that are fetched (a target row each, and a draft row for
+// the 164 sequences with a refusal), of which the sums kernel takes 76 at 5.6;
+// 8 sequences of 32003: 17.9 us, the two launches and a chain of small loads.
 #include <climits>
 #include <cmath>
 
