@@ -53,7 +53,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// 8 consecutive accumulator registers as one bf16 MFMA operand.
+// 8 consecutive accumulator registers as one bf16 MFMA operand.  So the
+// probabilities enter the second product, each off by at most 2^-8 of itself, no
+// more than the output's own rounding; a pair of high and low parts would double
+// the products that bound these kernels.  Their sum is taken before the rounding.
 template <int kFrom>
 __device__ __forceinline__ bf16x8 pack8(const f32x16& s) {
     u32x4 r;
