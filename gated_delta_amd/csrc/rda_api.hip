@@ -46,16 +46,29 @@ size_t rows_bytes(int64_t rows, int64_t stride, int64_t width) {
     return rows > 0 ? (size_t(rows - 1) * size_t(stride) + size_t(width)) * 2 : 0;
 }
 
+// (page_stride counts values of `row` a row; 16 bytes are `step` of them)
 rda_status check_pages(int64_t page_stride, int32_t num_pages, int32_t page_tokens,
-                       int32_t table_width) {
+                       int32_t table_width, int32_t row = RDA_MLA_ROW, int32_t step = 8) {
     if (num_pages < 0 || table_width < 0 || page_tokens < 1) return RDA_ERR_SHAPE;
     if (page_tokens < RDA_MLA_MIN_PAGE || page_tokens > RDA_MLA_MAX_PAGE ||
         (page_tokens & (page_tokens - 1)))
         return RDA_ERR_UNSUPPORTED;
-    if (page_stride < int64_t(page_tokens) * RDA_MLA_ROW || page_stride % 8 ||
+    if (page_stride < int64_t(page_tokens) * row || page_stride % step ||
         page_stride > (int64_t(1) << 40))
         return RDA_ERR_SHAPE;
     return RDA_OK;
+}
+
+rda_status check_pages_q4(int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                          int32_t table_width) {
+    return check_pages(page_stride, num_pages, page_tokens, table_width, RDA_MLA_ROW_Q4, 16);
+}
+
+// The bytes of a 4-bit cache.
+Range q4_range(const void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens) {
+    return rng(cache, num_pages > 0 ? size_t(num_pages - 1) * size_t(page_stride) +
+                                          size_t(page_tokens) * RDA_MLA_ROW_Q4
+                                    : 0);
 }
 
 // Query rows and tiles (of 32 cached rows, for 32 query rows or more) are
@@ -82,11 +95,12 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // sums (64 KiB per 32 rows) than in tiles (36 KiB each).  2 instead of 4: 8 x
 // 270 rows x 80 query rows 26 us for 28, but 7 sequences of 950 rows 22.5 for
 // 20.5 and one of 777 rows 21 for 20.
-size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
+// tile: cached rows per tile of the kernel.
+size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, int32_t tile = 32) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
     A.row_waves = unit_rows > 64 ? 4 : unit_rows > 32 ? 2 : 1;
     A.row_blocks = int32_t((unit_rows + 32 * A.row_waves - 1) / (32 * A.row_waves));
-    A.min_tiles = 4;   // (and no more than an average unit has: see the kernel)
+    A.min_tiles = 128 / tile;   // (and no more than an average unit has: see the kernel)
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* p = ws ? ws + at : nullptr;
@@ -106,12 +120,13 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
         // blocks of 128 rows once they fill the chip with long shares, or half of it
         // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
         // blocks of 32, whose four waves share out the tiles
-        const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
+        const int64_t tiles = (int64_t(A.prefix_len) + tile - 1) / tile;
         const int64_t blocks = (rows + 127) / 128;
-        A.prefix_waves = blocks * tiles >= 8 * kMlaWorkgroups || 2 * blocks >= kMlaWorkgroups ? 4 : 1;
+        A.prefix_waves =
+            blocks * tiles * tile >= 256 * kMlaWorkgroups || 2 * blocks >= kMlaWorkgroups ? 4 : 1;
         A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
         const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
-        const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
+        const int64_t least = tiles < 256 / tile ? tiles : 256 / tile;   // (no more than a block has)
         A.prefix_per = int32_t(share > least ? share : least);
         A.pre_bad = reinterpret_cast<int32_t*>(
             take((size_t(A.prefix_units) + kMlaWorkgroups) * sizeof(int32_t)));
@@ -120,6 +135,126 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws) {
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));
     }
     return at;
+}
+
+size_t mla_decode_bytes(int32_t batch, int32_t tokens, int32_t num_heads, int32_t prefix_len, int32_t tile) {
+    MlaDecodeArgs A{};
+    if (check_mla_decode_sizes(batch, tokens, num_heads, prefix_len) != RDA_OK) return 0;
+    A.batch = batch;
+    A.tokens = tokens;
+    A.heads = num_heads;
+    A.prefix_len = prefix_len;
+    return mla_decode_plan(A, nullptr, tile);
+}
+
+// rda_mla_decode and, with q4, rda_mla_decode_q4 (page_stride in bytes).
+rda_status mla_decode_any(bool q4, const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
+                          int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                          const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
+                          int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (rda_status st = check_mla_decode_sizes(batch, tokens, num_heads, prefix_len); st != RDA_OK)
+        return st;
+    // the combine kernel: four query rows a workgroup
+    if ((int64_t(batch) * tokens * num_heads + 3) / 4 >= kMaxWorkgroups) return RDA_ERR_SHAPE;
+    if (rda_status st = q4 ? check_pages_q4(page_stride, num_pages, page_tokens, table_width)
+                           : check_pages(page_stride, num_pages, page_tokens, table_width);
+        st != RDA_OK)
+        return st;
+    if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
+    // row numbers are 32 bits in the kernel, those of the tiles that it fetches
+    // (as zeros) behind the last too: up to nine tiles of 32
+    if (int64_t(table_width) * page_tokens > (int64_t(1) << 31) - 1024 ||
+        !mla_tiles_ok((int64_t(tokens) * num_heads + 31) / 32 * 32 * batch,
+                      int64_t(table_width) * page_tokens))
+        return RDA_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return RDA_ERR_VALUE;
+    if (batch == 0 || tokens == 0) return RDA_OK;
+    if (!q || !o || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache) ||
+        (prefix_len > 0 && !prefix_table))
+        return RDA_ERR_NULL;
+    for (const void* p : {q, cache, static_cast<const void*>(o)})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(kv_lens),
+                          static_cast<const void*>(prefix_table), static_cast<const void*>(lse)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    MlaDecodeArgs A{};
+    A.batch = batch;
+    A.tokens = tokens;
+    A.heads = num_heads;
+    A.prefix_len = prefix_len;
+    const int32_t tile = q4 ? 64 : 32;
+    const size_t need = mla_decode_plan(A, nullptr, tile);
+    if (!workspace || workspace_bytes < need) return RDA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return RDA_ERR_ALIGN;
+    mla_decode_plan(A, static_cast<unsigned char*>(workspace), tile);
+    const size_t rows = size_t(batch) * tokens * num_heads;
+    const Range in[] = {rng(q, rows * RDA_MLA_ROW * 2),
+                        q4 ? q4_range(cache, page_stride, num_pages, page_tokens)
+                           : rng(cache, rows_bytes(num_pages, page_stride, int64_t(page_tokens) * RDA_MLA_ROW)),
+                        rng(block_table, size_t(batch) * table_width * 4), rng(kv_lens, size_t(batch) * 4),
+                        rng(prefix_table, (size_t(prefix_len) + page_tokens - 1) / page_tokens * 4)};
+    const Range out[] = {rng(o, rows * RDA_MLA_LATENT * 2), rng(lse, rows * 4), rng(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(out[i], r)) return RDA_ERR_ALIAS;
+        if (overlap(out[i], out[(i + 1) % 3])) return RDA_ERR_ALIAS;
+    }
+    A.q = static_cast<const uint16_t*>(q);
+    A.cache = static_cast<const uint16_t*>(cache);
+    A.page_stride = page_stride;
+    A.num_pages = num_pages;
+    A.page_shift = __builtin_ctz(unsigned(page_tokens));
+    A.table = block_table;
+    A.table_width = table_width;
+    A.kv_lens = kv_lens;
+    A.prefix_table = prefix_table;
+    A.scale = scale;
+    A.o = static_cast<uint16_t*>(o);
+    A.lse = lse;
+    return (q4 ? launch_mla_decode_q4(A, stream) : launch_mla_decode(A, stream)) == hipSuccess
+               ? RDA_OK
+               : RDA_ERR_HIP;
+}
+
+// What rda_mla_append_q4 and rda_mla_read_q4 check alike; x, x_stride are the
+// rows outside the cache.
+rda_status check_rows_q4(const void* x, int64_t x_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+                         int32_t total_tokens, const int32_t* kv_lens, const int32_t* block_table,
+                         int32_t table_width, const void* cache, int64_t page_stride,
+                         int32_t num_pages, int32_t page_tokens) {
+    if (num_seqs < 1 || total_tokens < 0 || total_tokens > (1 << 25) ||
+        (!cu_seqlens && total_tokens % num_seqs))
+        return RDA_ERR_SHAPE;
+    if (!stride_ok(x_stride, RDA_MLA_ROW)) return RDA_ERR_SHAPE;
+    if (rda_status st = check_pages_q4(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
+        return st;
+    if (total_tokens == 0) return RDA_OK;
+    if (!x || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache))
+        return RDA_ERR_NULL;
+    for (const void* p : {x, cache})
+        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(cu_seqlens), static_cast<const void*>(kv_lens),
+                          static_cast<const void*>(block_table)})
+        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
+    return RDA_OK;
+}
+
+MlaRowsQ4Args rows_q4(const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                      const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
+                      const void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens) {
+    MlaRowsQ4Args A{};
+    A.cu = cu_seqlens;
+    A.kv_lens = kv_lens;
+    A.table = block_table;
+    A.num_seqs = num_seqs;
+    A.total = total_tokens;
+    A.table_width = table_width;
+    A.cache = const_cast<unsigned char*>(static_cast<const unsigned char*>(cache));
+    A.page_stride = page_stride;
+    A.num_pages = num_pages;
+    A.page_shift = __builtin_ctz(unsigned(page_tokens));
+    return A;
 }
 
 constexpr int kWalkSlices = kD / 16;  // value-channel slices per (sequence, head)
@@ -1124,13 +1259,7 @@ rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int6
 
 size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
                                       int32_t prefix_len) {
-    MlaDecodeArgs A{};
-    if (check_mla_decode_sizes(batch, tokens, num_heads, prefix_len) != RDA_OK) return 0;
-    A.batch = batch;
-    A.tokens = tokens;
-    A.heads = num_heads;
-    A.prefix_len = prefix_len;
-    return mla_decode_plan(A, nullptr);
+    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, 32);
 }
 
 rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
@@ -1138,62 +1267,25 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
                           const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
                           int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
                           float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-    if (rda_status st = check_mla_decode_sizes(batch, tokens, num_heads, prefix_len); st != RDA_OK)
-        return st;
-    // the combine kernel: four query rows a workgroup
-    if ((int64_t(batch) * tokens * num_heads + 3) / 4 >= kMaxWorkgroups) return RDA_ERR_SHAPE;
-    if (rda_status st = check_pages(page_stride, num_pages, page_tokens, table_width); st != RDA_OK)
-        return st;
-    if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
-    // row numbers are 32 bits in the kernel, those of the tiles that it fetches
-    // (as zeros) behind the last too: up to nine tiles of 32
-    if (int64_t(table_width) * page_tokens > (int64_t(1) << 31) - 1024 ||
-        !mla_tiles_ok((int64_t(tokens) * num_heads + 31) / 32 * 32 * batch,
-                      int64_t(table_width) * page_tokens))
-        return RDA_ERR_SHAPE;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return RDA_ERR_VALUE;
-    if (batch == 0 || tokens == 0) return RDA_OK;
-    if (!q || !o || !kv_lens || (table_width > 0 && !block_table) || (num_pages > 0 && !cache) ||
-        (prefix_len > 0 && !prefix_table))
-        return RDA_ERR_NULL;
-    for (const void* p : {q, cache, static_cast<const void*>(o)})
-        if (p && !aligned16(p)) return RDA_ERR_ALIGN;
-    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(kv_lens),
-                          static_cast<const void*>(prefix_table), static_cast<const void*>(lse)})
-        if (p && !aligned4(p)) return RDA_ERR_ALIGN;
-    MlaDecodeArgs A{};
-    A.batch = batch;
-    A.tokens = tokens;
-    A.heads = num_heads;
-    A.prefix_len = prefix_len;
-    const size_t need = mla_decode_plan(A, nullptr);
-    if (!workspace || workspace_bytes < need) return RDA_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return RDA_ERR_ALIGN;
-    mla_decode_plan(A, static_cast<unsigned char*>(workspace));
-    const size_t rows = size_t(batch) * tokens * num_heads;
-    const Range in[] = {rng(q, rows * RDA_MLA_ROW * 2),
-                        rng(cache, rows_bytes(num_pages, page_stride, int64_t(page_tokens) * RDA_MLA_ROW)),
-                        rng(block_table, size_t(batch) * table_width * 4), rng(kv_lens, size_t(batch) * 4),
-                        rng(prefix_table, (size_t(prefix_len) + page_tokens - 1) / page_tokens * 4)};
-    const Range out[] = {rng(o, rows * RDA_MLA_LATENT * 2), rng(lse, rows * 4), rng(workspace, need)};
-    for (int i = 0; i < 3; ++i) {
-        for (const Range& r : in)
-            if (overlap(out[i], r)) return RDA_ERR_ALIAS;
-        if (overlap(out[i], out[(i + 1) % 3])) return RDA_ERR_ALIAS;
-    }
-    A.q = static_cast<const uint16_t*>(q);
-    A.cache = static_cast<const uint16_t*>(cache);
-    A.page_stride = page_stride;
-    A.num_pages = num_pages;
-    A.page_shift = __builtin_ctz(unsigned(page_tokens));
-    A.table = block_table;
-    A.table_width = table_width;
-    A.kv_lens = kv_lens;
-    A.prefix_table = prefix_table;
-    A.scale = scale;
-    A.o = static_cast<uint16_t*>(o);
-    A.lse = lse;
-    return launch_mla_decode(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+    return mla_decode_any(false, q, cache, page_stride, num_pages, page_tokens, block_table, table_width,
+                          kv_lens, prefix_table, prefix_len, batch, tokens, num_heads, scale, o, lse,
+                          workspace, workspace_bytes, stream);
+}
+
+size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
+                                         int32_t prefix_len) {
+    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, 64);
+}
+
+rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
+                             int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                             const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
+                             int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    return mla_decode_any(true, q, cache, page_stride, num_pages, page_tokens, block_table, table_width,
+                          kv_lens, prefix_table, prefix_len, batch, tokens, num_heads, scale, o, lse,
+                          workspace, workspace_bytes, stream);
 }
 
 rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight, float eps,
@@ -1239,6 +1331,55 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
     A.num_pages = num_pages;
     A.page_shift = __builtin_ctz(unsigned(page_tokens));
     return launch_mla_append(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+}
+
+rda_status rda_mla_append_q4(const void* kv, int64_t kv_stride, const float* weight, float eps,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                             const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
+                             void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                             hipStream_t stream) {
+    if (rda_status st = check_rows_q4(kv, kv_stride, cu_seqlens, num_seqs, total_tokens, kv_lens, block_table,
+                                      table_width, cache, page_stride, num_pages, page_tokens);
+        st != RDA_OK)
+        return st;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return RDA_ERR_VALUE;
+    if (total_tokens == 0) return RDA_OK;
+    if (weight && !aligned16(weight)) return RDA_ERR_ALIGN;
+    const Range rc = q4_range(cache, page_stride, num_pages, page_tokens);
+    for (const Range& r : {rng(kv, rows_bytes(total_tokens, kv_stride, RDA_MLA_ROW)),
+                           rng(weight, RDA_MLA_LATENT * 4), rng(cu_seqlens, (size_t(num_seqs) + 1) * 4),
+                           rng(kv_lens, size_t(num_seqs) * 4),
+                           rng(block_table, size_t(num_seqs) * table_width * 4)})
+        if (overlap(rc, r)) return RDA_ERR_ALIAS;
+    if (num_pages == 0 || table_width == 0) return RDA_OK;
+    MlaRowsQ4Args A = rows_q4(cu_seqlens, num_seqs, total_tokens, kv_lens, block_table, table_width, cache,
+                              page_stride, num_pages, page_tokens);
+    A.kv = static_cast<const uint16_t*>(kv);
+    A.kv_stride = kv_stride;
+    A.weight = weight;
+    A.eps = eps;
+    return launch_mla_append_q4(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
+}
+
+rda_status rda_mla_read_q4(const void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                           const int32_t* block_table, int32_t table_width, const int32_t* kv_lens,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, void* out,
+                           int64_t out_stride, hipStream_t stream) {
+    if (rda_status st = check_rows_q4(out, out_stride, cu_seqlens, num_seqs, total_tokens, kv_lens, block_table,
+                                      table_width, cache, page_stride, num_pages, page_tokens);
+        st != RDA_OK)
+        return st;
+    if (total_tokens == 0) return RDA_OK;
+    const Range ro = rng(out, rows_bytes(total_tokens, out_stride, RDA_MLA_ROW));
+    for (const Range& r : {q4_range(cache, page_stride, num_pages, page_tokens),
+                           rng(cu_seqlens, (size_t(num_seqs) + 1) * 4), rng(kv_lens, size_t(num_seqs) * 4),
+                           rng(block_table, size_t(num_seqs) * table_width * 4)})
+        if (overlap(ro, r)) return RDA_ERR_ALIAS;
+    MlaRowsQ4Args A = rows_q4(cu_seqlens, num_seqs, total_tokens, kv_lens, block_table, table_width, cache,
+                              page_stride, num_pages, page_tokens);
+    A.out = static_cast<uint16_t*>(out);
+    A.out_stride = out_stride;
+    return launch_mla_read_q4(A, stream) == hipSuccess ? RDA_OK : RDA_ERR_HIP;
 }
 
 size_t rda_verify_drafts_workspace_bytes(int32_t batch, int32_t vocab) {

@@ -376,6 +376,29 @@ struct MlaAppendArgs {
 };
 hipError_t launch_mla_append(const MlaAppendArgs& A, hipStream_t stream);
 
+// The same over a cache of 4-bit rows: MlaDecodeArgs with cache the pages'
+// bytes and page_stride in bytes.
+hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream);
+
+// Rows into the 4-bit cache (kv, weight, eps) or out of it (out).
+struct MlaRowsQ4Args {
+    const uint16_t* kv;          // [T] rows of kv_stride values
+    int64_t kv_stride;
+    const float* weight;         // [512] or nullptr (no norm)
+    float eps;
+    uint16_t* out;               // [T] rows of out_stride values
+    int64_t out_stride;
+    const int32_t* cu;           // [N+1] or nullptr (N sequences of equal length)
+    const int32_t* kv_lens;      // [N] rows of each sequence, the call's last
+    const int32_t* table;        // [N, table_width]
+    int32_t num_seqs, total, table_width;
+    unsigned char* cache;        // pages of page_stride bytes
+    int64_t page_stride;
+    int32_t num_pages, page_shift;
+};
+hipError_t launch_mla_append_q4(const MlaRowsQ4Args& A, hipStream_t stream);
+hipError_t launch_mla_read_q4(const MlaRowsQ4Args& A, hipStream_t stream);
+
 // Verification of drafted tokens.
 constexpr int kVerifyChunk = 4096;   // tokens of the vocabulary per partial sum
 struct VerifyArgs {

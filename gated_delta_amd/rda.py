@@ -31,7 +31,7 @@ RDA_GATE_SIGMOID, RDA_GATE_SILU, RDA_GATE_NONE = 0, 1, 2
 RDA_CONV_MAX_WIDTH = 4
 RDA_MLA_NOPE, RDA_MLA_PE, RDA_MLA_QK = 128, 64, 192
 RDA_MLA_V, RDA_MLA_KV = 128, 256
-RDA_MLA_LATENT, RDA_MLA_ROW = 512, 576
+RDA_MLA_LATENT, RDA_MLA_ROW, RDA_MLA_ROW_Q4 = 512, 576, 400
 RDA_MLA_MIN_PAGE, RDA_MLA_MAX_PAGE = 8, 65536
 RDA_CONV_ACT_NONE, RDA_CONV_ACT_SILU = 0, 1
 _CONV_ACTS = {"none": RDA_CONV_ACT_NONE, "silu": RDA_CONV_ACT_SILU}
@@ -116,6 +116,14 @@ def _load():
         lib.rda_mla_decode.restype = ctypes.c_int
         lib.rda_mla_append.argtypes = [p, i64, p, f32, p, i32, i32, p, p, i32, p, i64, i32, i32, p]
         lib.rda_mla_append.restype = ctypes.c_int
+        lib.rda_mla_append_q4.argtypes = lib.rda_mla_append.argtypes
+        lib.rda_mla_append_q4.restype = ctypes.c_int
+        lib.rda_mla_read_q4.argtypes = [p, i64, i32, i32, p, i32, p, p, i32, i32, p, i64, p]
+        lib.rda_mla_read_q4.restype = ctypes.c_int
+        lib.rda_mla_decode_q4_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.rda_mla_decode_q4_workspace_bytes.restype = sz
+        lib.rda_mla_decode_q4.argtypes = lib.rda_mla_decode.argtypes
+        lib.rda_mla_decode_q4.restype = ctypes.c_int
         lib.rda_verify_drafts_workspace_bytes.argtypes = [i32, i32]
         lib.rda_verify_drafts_workspace_bytes.restype = sz
         lib.rda_verify_drafts.argtypes = [p, i64, p, i64, p, p, p, i32, i32, i32, p, p, p, sz, p]
@@ -593,28 +601,16 @@ def _need_cache(cache: torch.Tensor, dev) -> int:
                       (cache.shape[0], cache.shape[1], RDA_MLA_ROW), dev)
 
 
-def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
-                   kv_lens: torch.Tensor, scale: float, *,
-                   prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
-                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                   want_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
-    """Absorbed latent attention over a paged cache (C entry point
-    ``rda_mla_decode``).
-
-    q [B, T, H, 576] bf16, cache [pages, page_tokens, 576] bf16 (pages may be
-    further apart), block_table [B, width] int32, kv_lens [B] int32 (rows of
-    each sequence, the T new ones included), optionally prefix_table int32
-    and prefix_len: rows that the whole batch shares and sees.  All on the
-    device, never copied to the host.  Returns (o [B, T, H, 512] bf16, lse
-    [B, T, H] fp32 or None).
-    """
+def _mla_decode(name, need_cache, workspace_bytes, q, cache, block_table, kv_lens, scale, prefix_table,
+                prefix_len, o, lse, want_lse, workspace, stream):
+    """rda_mla_decode and rda_mla_decode_q4."""
     lib_ = _load()
     dev = _need_gpu(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, 576]")
     B, T, H, _ = q.shape
     _need(q, "q", torch.bfloat16, (B, T, H, RDA_MLA_ROW), dev)
-    page_stride = _need_cache(cache, dev)
+    page_stride = need_cache(cache, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, width]")
     _need(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev)
@@ -633,17 +629,93 @@ def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tens
         lse = _empty((B, T, H), torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, T, H), dev)
-    workspace = _scratch(workspace, rda_mla_decode_workspace_bytes(B, T, H, max(prefix_len, 0)), dev, stream)
+    workspace = _scratch(workspace, workspace_bytes(B, T, H, max(prefix_len, 0)), dev, stream)
     with _On(dev):
-        st = lib_.rda_mla_decode(_addr(q), _addr(cache), page_stride, cache.shape[0], cache.shape[1],
+        st = getattr(lib_, name)(_addr(q), _addr(cache), page_stride, cache.shape[0], cache.shape[1],
                                  _addr(block_table), block_table.shape[1], _addr(kv_lens),
                                  _addr(prefix_table) if prefix_len > 0 else None, prefix_len, B, T,
                                  H, float(scale), _addr(o), _addr(lse), _addr(workspace),
                                  workspace.numel() * workspace.element_size(),
                                  _stream_on(dev, stream))
     if st != 0:
-        raise RdaError(st, "rda_mla_decode")
+        raise RdaError(st, name)
     return o, lse
+
+
+def rda_mla_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                   kv_lens: torch.Tensor, scale: float, *,
+                   prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   want_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed latent attention over a paged cache (C entry point
+    ``rda_mla_decode``).
+
+    q [B, T, H, 576] bf16, cache [pages, page_tokens, 576] bf16 (pages may be
+    further apart), block_table [B, width] int32, kv_lens [B] int32 (rows of
+    each sequence, the T new ones included), optionally prefix_table int32
+    and prefix_len: rows that the whole batch shares and sees.  All on the
+    device, never copied to the host.  Returns (o [B, T, H, 512] bf16, lse
+    [B, T, H] fp32 or None).
+    """
+    return _mla_decode("rda_mla_decode", _need_cache, rda_mla_decode_workspace_bytes, q, cache, block_table,
+                       kv_lens, scale, prefix_table, prefix_len, o, lse, want_lse, workspace, stream)
+
+
+def _need_cache_q4(cache: torch.Tensor, dev) -> int:
+    """The pages of a 4-bit cache; their distance in bytes."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be [pages, page_tokens, 400]")
+    return _need_rows(cache, "cache", torch.uint8,
+                      (cache.shape[0], cache.shape[1], RDA_MLA_ROW_Q4), dev)
+
+
+@functools.lru_cache(maxsize=256)
+def rda_mla_decode_q4_workspace_bytes(batch: int, tokens: int, num_heads: int,
+                                      prefix_len: int = 0) -> int:
+    return int(_load().rda_mla_decode_q4_workspace_bytes(int(batch), int(tokens), int(num_heads),
+                                                         int(prefix_len)))
+
+
+def rda_mla_decode_q4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                      kv_lens: torch.Tensor, scale: float, *,
+                      prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                      o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      want_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Absorbed latent attention over a 4-bit cache (C entry point
+    ``rda_mla_decode_q4``): cache [pages, page_tokens, 400] uint8 as
+    rda_mla_append_q4 writes it, everything else as in rda_mla_decode."""
+    return _mla_decode("rda_mla_decode_q4", _need_cache_q4, rda_mla_decode_q4_workspace_bytes, q, cache, block_table,
+                       kv_lens, scale, prefix_table, prefix_len, o, lse, want_lse, workspace, stream)
+
+
+def _mla_append(name, need_cache, kv, cache, block_table, kv_lens, cu_seqlens, weight, eps, stream):
+    """rda_mla_append and rda_mla_append_q4."""
+    lib_ = _load()
+    dev = _need_gpu(kv, "kv")
+    if kv.dim() != 2:
+        raise ValueError("kv must be [T, 576]")
+    T = kv.shape[0]
+    stride = _need_rows(kv, "kv", torch.bfloat16, (T, RDA_MLA_ROW), dev)
+    page_stride = need_cache(cache, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [N, width]")
+    N = block_table.shape[0]
+    _need(block_table, "block_table", torch.int32, (N, block_table.shape[1]), dev)
+    _need(kv_lens, "kv_lens", torch.int32, (N,), dev)
+    cu = _offsets(cu_seqlens, "cu_seqlens", T, dev, stream)
+    if cu is not None and cu.numel() != N + 1:
+        raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (RDA_MLA_LATENT,), dev)
+    with _On(dev):
+        st = getattr(lib_, name)(_addr(kv), stride, _addr(weight), float(eps), _addr(cu), N, T,
+                                 _addr(kv_lens), _addr(block_table), block_table.shape[1],
+                                 _addr(cache), page_stride, cache.shape[0], cache.shape[1],
+                                 _stream_on(dev, stream))
+    if st != 0:
+        raise RdaError(st, name)
+    return cache
 
 
 def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -658,13 +730,40 @@ def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     rda_mla_prefill's cu_q, or None for sequences of equal length; weight
     [512] fp32 or None (no norm).  Returns cache.
     """
+    return _mla_append("rda_mla_append", _need_cache, kv, cache, block_table, kv_lens, cu_seqlens, weight,
+                       eps, stream)
+
+
+def rda_mla_append_q4(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                      kv_lens: torch.Tensor, cu_seqlens=None, *,
+                      weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                      stream=None) -> torch.Tensor:
+    """New rows into the 4-bit latent cache (C entry point
+    ``rda_mla_append_q4``): cache [pages, page_tokens, 400] uint8, everything
+    else as in rda_mla_append.  Returns cache."""
+    return _mla_append("rda_mla_append_q4", _need_cache_q4, kv, cache, block_table, kv_lens, cu_seqlens,
+                       weight, eps, stream)
+
+
+def rda_mla_read_q4(cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                    total_tokens: int, cu_seqlens=None, *, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Rows of the 4-bit latent cache in bf16 (C entry point ``rda_mla_read_q4``).
+
+    cache, block_table [N, width], kv_lens [N] as rda_mla_append_q4 takes them;
+    cu_seqlens: offsets of each sequence's rows in the result, or None for equal
+    parts of total_tokens: a sequence's part holds the last of its kv_lens rows.
+    Returns out [total_tokens, 576] bf16 (rows contiguous, any multiple of 8
+    elements apart); rows behind the last offset are left as they are.
+    """
     lib_ = _load()
-    dev = _need_gpu(kv, "kv")
-    if kv.dim() != 2:
-        raise ValueError("kv must be [T, 576]")
-    T = kv.shape[0]
-    stride = _need_rows(kv, "kv", torch.bfloat16, (T, RDA_MLA_ROW), dev)
-    page_stride = _need_cache(cache, dev)
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    dev = _need_gpu(cache, "cache")
+    page_stride = _need_cache_q4(cache, dev)
+    T = int(total_tokens)
+    if T < 0:
+        raise ValueError("total_tokens must not be negative")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [N, width]")
     N = block_table.shape[0]
@@ -673,16 +772,16 @@ def rda_mla_append(kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     cu = _offsets(cu_seqlens, "cu_seqlens", T, dev, stream)
     if cu is not None and cu.numel() != N + 1:
         raise ValueError("cu_seqlens must have one entry more than block_table has rows")
-    if weight is not None:
-        _need(weight, "weight", torch.float32, (RDA_MLA_LATENT,), dev)
+    if out is None:
+        out = _empty((T, RDA_MLA_ROW), torch.bfloat16, dev, stream)
+    stride = _need_rows(out, "out", torch.bfloat16, (T, RDA_MLA_ROW), dev)
     with _On(dev):
-        st = lib_.rda_mla_append(_addr(kv), stride, _addr(weight), float(eps), _addr(cu), N, T,
-                                 _addr(kv_lens), _addr(block_table), block_table.shape[1],
-                                 _addr(cache), page_stride, cache.shape[0], cache.shape[1],
-                                 _stream_on(dev, stream))
+        st = lib_.rda_mla_read_q4(_addr(cache), page_stride, cache.shape[0], cache.shape[1],
+                                  _addr(block_table), block_table.shape[1], _addr(kv_lens), _addr(cu), N,
+                                  T, _addr(out), stride, _stream_on(dev, stream))
     if st != 0:
-        raise RdaError(st, "rda_mla_append")
-    return cache
+        raise RdaError(st, "rda_mla_read_q4")
+    return out
 
 
 @functools.lru_cache(maxsize=256)

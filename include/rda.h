@@ -73,6 +73,7 @@ extern "C" {
 #define RDA_MLA_KV 256      /* expanded keys and values of a head: NOPE + V */
 #define RDA_MLA_LATENT 512  /* the latent vector */
 #define RDA_MLA_ROW 576     /* a cached row, and an absorbed query: LATENT + PE */
+#define RDA_MLA_ROW_Q4 400  /* bytes of a cached row in 4 bits */
 #define RDA_MLA_MIN_PAGE 8       /* rows of a cache page: a power of two */
 #define RDA_MLA_MAX_PAGE 65536
 
@@ -601,6 +602,77 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
                           const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
                           void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
                           hipStream_t stream);
+
+/*
+ * The latent cache in 4 bits: 400 bytes a cached row instead of 1152, for
+ * contexts that would not fit, or for less to read per token.  A row holds
+ *
+ *   bytes [0, 256)    the 512 latent values as e2m1 codes, channel c in byte
+ *                     c / 2, an even one in the low half: 0, 0.5, 1, 1.5, 2,
+ *                     3, 4, 6 for the codes 0 .. 7, negative with bit 3
+ *   bytes [256, 272)  a scale byte s for each 32 channels, whose values are
+ *                     the codes' times 2^(s - 127); 255: all 32 are NaN
+ *   bytes [272, 400)  the 64 shared key channels in bf16
+ *
+ * and a page of page_tokens rows (as in rda_mla_decode) lies page_stride bytes
+ * after the one before (a multiple of 16, at least page_tokens x 400).
+ *
+ * rda_mla_append_q4 writes it, with rda_mla_append's norm and places:
+ *
+ *     y_c  = x_c / sqrt(mean_{c' < 512} x_c'^2 + eps) * weight_c, or x_c
+ *     e    = the least integer with |y_c| <= 7 2^e in the 32 channels, no
+ *            less than -120 and no more than 125 (s = e + 127)
+ *     code = y_c / 2^e rounded to nearest (ties to the even code, the largest
+ *            is 6)
+ *
+ * where y, e and the rounding are computed in 64 bits.  No value moves further
+ * than half a step between neighbouring codes of its group.  32 channels among which
+ * y holds an infinity or NaN become NaN.  Arguments and errors as in rda_mla_append.
+ */
+rda_status rda_mla_append_q4(const void* kv, int64_t kv_stride, const float* weight, float eps,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                             const int32_t* kv_lens, const int32_t* block_table, int32_t table_width,
+                             void* cache, int64_t page_stride, int32_t num_pages, int32_t page_tokens,
+                             hipStream_t stream);
+
+/*
+ * Rows of the 4-bit cache as the bf16 values that they stand for (exact),
+ * packed by sequence: what a prompt that comes in pieces up-projects again for
+ * rda_mla_prefill.  The counterpart of rda_mla_append_q4: row i of sequence n's
+ * part of `out` is the cached row at position kv_lens[n] - (rows of the part) + i,
+ * so all of a sequence where its part has kv_lens[n] rows.
+ *
+ *   cu_seqlens  device int32 [num_seqs + 1] offsets of the parts, or NULL for
+ *               num_seqs parts of equal length (total_tokens at most 2^25)
+ *   out         [total_tokens] rows out_stride values apart (a multiple of 8,
+ *               at least 576) of 576 bf16 values; may not overlap the rest
+ * A row whose position or page id is out of range is zeros; rows outside every
+ * part are left as they are.
+ */
+rda_status rda_mla_read_q4(const void* cache, int64_t page_stride, int32_t num_pages,
+                           int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                           const int32_t* kv_lens, const int32_t* cu_seqlens, int32_t num_seqs,
+                           int32_t total_tokens, void* out, int64_t out_stride, hipStream_t stream);
+
+/* Workspace bytes rda_mla_decode_q4 needs (0 on bad sizes); as
+ * rda_mla_decode_workspace_bytes. */
+size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
+                                         int32_t prefix_len);
+
+/*
+ * rda_mla_decode over the 4-bit cache (page_stride in bytes; every other
+ * argument, limit and error as there).  The query is used as it is: in the
+ * products with the codes it is a pair of 8-bit values with scales of the
+ * row's largest magnitude, together off by at most 2^-21 of that.  A query row
+ * whose latent part holds an infinity or NaN, and one that sees a row with a
+ * NaN group, gives NaN throughout; rows that it does not see do not reach it.
+ */
+rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
+                             int32_t page_tokens, const int32_t* block_table, int32_t table_width,
+                             const int32_t* kv_lens, const int32_t* prefix_table, int32_t prefix_len,
+                             int32_t batch, int32_t tokens, int32_t num_heads, float scale, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
 
 /* Workspace bytes rda_verify_drafts needs (0 on bad sizes); no
  * initialisation, one per call that may overlap another. */
