@@ -12,30 +12,31 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kJoinThreads = 256;
 constexpr int kTile = 64;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 25600
-constexpr int kWaveRows = 16;                    // rows of a tile that a wave fetches
-constexpr int kWaveBytes = kWaveRows * kQ4Row;   // 6400
-constexpr int kDma = 7;                          // transfers for them: 400 granules of 16 bytes
+constexpr int kWaveRows = kTile / kWaves;        // rows of a tile that a wave fetches
+constexpr int kWaveBytes = kWaveRows * kQ4Row;
 constexpr int kValRows = 32;                     // rows unpacked at a time
-constexpr int kValBytes = kValRows * 256;        // of 128 channels
+constexpr int kValChannels = kMlaLatent / kWaves;
+constexpr int kValRow = kValChannels * 2;        // bytes
+constexpr int kValBytes = kValRows * kValRow;
 constexpr int kPieceTiles = 3;
-
-__device__ const __attribute__((aligned(16))) uint32_t kZeros[4] = {};
 
 template <int kRW>
 struct Lds {
     static constexpr int kBuf = kRW == 4 ? 3 : 4;   // tiles in flight or in use
     unsigned char tile[kBuf][kTileBytes];
-    unsigned char val[4][kValBytes];     // a wave's own: unpacked values, 128 channels
-    u32x4 p[2][kRW][4][64];              // probabilities: [row block][16 cached rows][lane]
-    float top[4][32];
-    float l[4][32];
+    unsigned char val[kWaves][kValBytes];   // a wave's own: unpacked values of its channels
+    u32x4 p[2][kRW][kTile / 16][64];        // probabilities: [32 query rows][16 cached rows][lane]
+    float top[kWaves][16];
+    float l[kWaves][16];
     float mu[kRW * 32];
     float factor[kRW * 32];
     int moved[3];
-    int scan[8];
+    int scan[2 * kWaves];
     int unit, first;
 };
 
@@ -78,10 +79,10 @@ __device__ __forceinline__ void lds_write_u4(uint32_t a, u32x4 x) {
     *(lds_u32x4*)(lds_char*)uintptr_t(a) = x;
 }
 
-// Row r of unpacked values keeps 16-byte granule j at j ^ val_swz(r): sixteen
-// rows written at one granule, and the rows and granules that a transposing
-// read touches at a time, fall on distinct banks.
-__device__ __forceinline__ int val_swz(int r) { return (r & 3) << 2 | (r >> 3 & 1) << 1 | (r >> 2 & 1); }
+// Row r of unpacked values (128 bytes) keeps 16-byte granule j at j ^ val_swz(r):
+// sixteen rows written at one granule, and the rows and granules that a
+// transposing read touches at a time, fall on distinct banks.
+__device__ __forceinline__ int val_swz(int r) { return (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1 | (r >> 2 & 1); }
 
 __device__ __forceinline__ int clamp_len(const MlaDecodeArgs& A, int b) {
     const int64_t most = int64_t(A.table_width) << A.page_shift;
@@ -97,36 +98,6 @@ struct Source {
 __device__ __forceinline__ int page_of(const MlaDecodeArgs& A, const Source& src, int k) {
     const int at = k < src.len ? k >> A.page_shift : 0;
     return src.len > 0 ? min(max(((const_i32*)src.table)[at], 0), A.num_pages - 1) : 0;
-}
-
-// Sixteen rows [k, k + 16) into LDS as they lie, one behind the other: two
-// groups of eight (a page holds whole groups of eight).  Rows from `end` on are
-// read as zeros.
-__device__ __forceinline__ void fetch_rows(const MlaDecodeArgs& A, const int (&page)[2], int k, int end,
-                                           uint32_t lds, int lane) {
-    const char* base[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-        base[n] = reinterpret_cast<const char*>(A.cache) + int64_t(page[n]) * A.page_stride +
-                  int64_t((k + 8 * n) & ((1 << A.page_shift) - 1)) * kQ4Row;
-    const int l = here(lane);
-    const int valid = end - k;
-    if (valid >= kWaveRows) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) dma16_at(base[0], 16 * l + 1024 * i, lds + 1024 * i);
-        dma16_from(l < 8 ? base[0] + 16 * l + 1024 * 3 : base[1] + 16 * l - 128, lds + 1024 * 3);
-#pragma unroll
-        for (int i = 4; i < 6; ++i) dma16_at(base[1], 16 * l + 1024 * i - 3200, lds + 1024 * i);
-        if (l < 16) dma16_at(base[1], 16 * l + 1024 * 6 - 3200, lds + 1024 * 6);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kDma; ++i) {
-            const int g = 64 * i + l, row = g * 5243 >> 17;   // g / 25
-            const char* from = g < 200 ? base[0] + 16 * g : base[1] + 16 * (g - 200);
-            if (row >= valid) from = reinterpret_cast<const char*>(kZeros);
-            if (i < kDma - 1 || l < 16) dma16_from(from, lds + 1024 * i);
-        }
-    }
 }
 
 // Where a piece's sums go: the outputs, or a slot of partial sums.
@@ -197,10 +168,11 @@ __device__ __forceinline__ void load_query(Query& Q, const uint16_t* row, int t)
 template <int kRW, bool kCausal>
 __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, const Source& src, int t0,
                                       int t1, const Sink& sink) {
-    constexpr int kKW = 4 / kRW, kTB = kRW;
+    constexpr int kRowWaves = 2 * kRW, kKW = kWaves / kRowWaves;   // row waves, key waves
+    constexpr int kTB = kTile / 16 / kKW;                          // blocks of 16 cached rows a wave scores
     constexpr int kBuf = Lds<kRW>::kBuf;
     const int w = wave_id(), l = threadIdx.x & 63;
-    const int rw = w % kRW, kw = w / kRW;
+    const int rw = w % kRowWaves, kw = w / kRowWaves;
     const int c16 = l & 15, t = l >> 4, c32 = l & 31, g = l >> 5;
     const int end = min(src.len, t1 * kTile);
     const int all_see = kCausal ? src.len - (A.tokens - 1) : src.len;
@@ -208,154 +180,142 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     const uint32_t tiles = lds_addr(&lds.tile[0][0]);
     const uint32_t val = lds_addr(&lds.val[w][0]);
 
-    int page[2];
-    auto pages = [&](int tile) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) page[n] = page_of(A, src, tile * kTile + kWaveRows * w + 8 * n);
-    };
+    int page;   // of this wave's rows of the next tile to fetch
     auto issue = [&](int tile, int buf) {
-        fetch_rows(A, page, tile * kTile + kWaveRows * w, end, tiles + buf * kTileBytes + w * kWaveBytes, l);
-        pages(tile + 1);
+        const int k = tile * kTile + kWaveRows * w;
+        q4_fetch_rows(reinterpret_cast<const char*>(A.cache) + int64_t(page) * A.page_stride +
+                          int64_t(k & ((1 << A.page_shift) - 1)) * kQ4Row,
+                      end - k, tiles + buf * kTileBytes + w * kWaveBytes, l);
+        page = page_of(A, src, k + kTile);
     };
-    pages(t0);
+    page = page_of(A, src, t0 * kTile + kWaveRows * w);
 #pragma unroll 1
     for (int d = 0; d < kBuf - 1; ++d) issue(t0 + d, d);
 
-    Query q[2];
-    int limit[2];
-    float m[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, lsum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-        const int row = min(32 * rw + 16 * nb + c16, sink.rows - 1);
-        load_query(q[nb], A.q + (sink.row0 + row) * kMlaRow, t);
-        limit[nb] = kCausal ? src.len - (A.tokens - 1 - (sink.first_row + row) / A.heads) : src.len;
-    }
-    f32x16 acc[kRW][4];
+    Query q;
+    float m = -INFINITY, mu = 0.f, lsum = 0.f;
+    const int qrow = min(16 * rw + c16, sink.rows - 1);
+    load_query(q, A.q + (sink.row0 + qrow) * kMlaRow, t);
+    const int limit = kCausal ? src.len - (A.tokens - 1 - (sink.first_row + qrow) / A.heads) : src.len;
+    f32x16 acc[kRW][2];
 #pragma unroll
     for (int rb = 0; rb < kRW; ++rb)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[rb][b][i] = 0.f;
 
     // this lane's addresses, from a tile's start
-    const uint32_t krow = (kw * kTB * 16 + c16) * kQ4Row;            // its row's scores
-    const uint32_t drow = c32 * kQ4Row;                              // the row it unpacks
+    const uint32_t krow = (kw * kTB * 16 + c16) * kQ4Row;                // the row it scores
+    const uint32_t drow = c32 * kQ4Row + kQ4ScaleAt / kWaves * w + 16 * g;   // its part of the row it unpacks
+    const uint32_t dscale = c32 * kQ4Row + kQ4ScaleAt + (2 * w & ~3);
+    const int dshift = 8 * ((2 * w & 3) + g);
+    const uint32_t vput = val + c32 * kValRow;
     const int vr = 8 * g + (c16 >> 2), vlow = 2 * (t & 1) + ((c16 >> 1) & 1);
-    uint32_t va[2];
+    uint32_t vget[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-        va[n] = val + (vr + 4 * n) * 256 + 16 * (vlow ^ val_swz(vr + 4 * n)) + 8 * (c16 & 1);
-    const bool idle = 32 * rw >= sink.rows;
-    const int row_blocks = min(kRW, (sink.rows + 31) / 32);
+        vget[n] = val + (vr + 4 * n) * kValRow + 16 * (vlow ^ val_swz(vr + 4 * n)) + 8 * (c16 & 1);
+    const uint32_t pput = lds_addr(&lds.p[0][rw >> 1][kw * kTB][16 * (rw & 1) + c16 + 32 * (t >> 1)]) + 8 * (t & 1);
+    const bool idle = 16 * rw >= sink.rows;
 
-    if constexpr (kKW == 1 || kRW == 2) {
-        wait_vm<(kBuf - 2) * kDma>();
-        raw_barrier();
-    }
+    wait_vm<(kBuf - 2) * kQ4Fetch>();
+    raw_barrier();
     const int n_tiles = t1 - t0;
     for (int i = 0; i < n_tiles; ++i) {
         const int k0 = (t0 + i) * kTile, buf = i % kBuf, flag = i % 3;
         const uint32_t tile = tiles + buf * kTileBytes;
-        if constexpr (kRW == 1) wait_vm<(kBuf - 2) * kDma>();   // its own 16 rows have landed
-        f32x4 s[kTB][2];
-        float p[2][2];   // (reference moves)
-        (void)p;
+        // 32 rows of this wave's 64 channels as bf16
+        auto unpack = [&](int ch) {
+            const uint32_t at = tile + ch * kValRows * kQ4Row;
+            const uint32_t sb = (lds_read4(at + dscale) >> dshift) & 255;
+            const u32x4 x = lds_read_u4(at + drow);
+            // NaN groups are left out here: they have made the scores of all who
+            // see them NaN, and no others may meet them as 0 x NaN
+            const float f = q4_scale(sb == kQ4Bad ? 0 : sb);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                lds_write_u4(vput + 16 * ((4 * g + j) ^ val_swz(c32)), q4_eight(x[j], f));
+        };
+        f32x4 s[kTB];
         auto store_p = [&]() {
 #pragma unroll
-            for (int tb = 0; tb < kTB; ++tb)
+            for (int tb = 0; tb < kTB; ++tb) {
+                f32x4 e;
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    f32x4 e;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        e[x] = __builtin_amdgcn_exp2f(fmaf(s[tb][nb][x], c, -mu[nb]));
-                        lsum[nb] += e[x];
-                    }
-                    const u32x2 y = {pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])};
-                    *reinterpret_cast<u32x2*>(
-                        reinterpret_cast<char*>(&lds.p[i & 1][rw][kw * kTB + tb][16 * nb + c16 + 32 * (t >> 1)]) +
-                        8 * (t & 1)) = y;
+                for (int x = 0; x < 4; ++x) {
+                    e[x] = __builtin_amdgcn_exp2f(fmaf(s[tb][x], c, -mu));
+                    lsum += e[x];
                 }
+                typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+                *(lds_u32x2*)(lds_char*)uintptr_t(pput + (i & 1) * sizeof(lds.p[0]) + tb * sizeof(lds.p[0][0][0])) =
+                    u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])};
+            }
         };
-        float top[2], before[2];
+        float top = -INFINITY, before = 0.f;
         if (!idle) {
 #pragma unroll
             for (int tb = 0; tb < kTB; ++tb) {
                 const uint32_t row = tile + krow + tb * 16 * kQ4Row;
                 const int sc = int(lds_read4(row + kQ4ScaleAt + 4 * t));
-                s[tb][0] = s[tb][1] = zero4();
+                s[tb] = zero4();
                 each<4>([&](auto mm) {
                     constexpr int n = decltype(mm)::value;
                     const u32x4 k4 = lds_read_u4(row + 64 * t + 16 * n);
-                    i32x8 a = {int(k4[0]), int(k4[1]), int(k4[2]), int(k4[3]), 0, 0, 0, 0};
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        s[tb][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            a, q[nb].hi[n], s[tb][nb], 4, 0, n, sc, 0, int(q[nb].scale));
-                        s[tb][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            a, q[nb].lo[n], s[tb][nb], 4, 0, n, sc, 1, int(q[nb].scale));
-                    }
+                    const i32x8 a = {int(k4[0]), int(k4[1]), int(k4[2]), int(k4[3]), 0, 0, 0, 0};
+                    s[tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.hi[n], s[tb], 4, 0, n, sc, 0,
+                                                                            int(q.scale));
+                    s[tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.lo[n], s[tb], 4, 0, n, sc, 1,
+                                                                            int(q.scale));
                 });
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const bf16x8 pe = lds_read16(row + kQ4PeAt + 64 * n + 16 * t);
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) s[tb][nb] = mfma_bf16(pe, q[nb].pe[n], s[tb][nb]);
-                }
+                for (int n = 0; n < 2; ++n)
+                    s[tb] = mfma_bf16(lds_read16(row + kQ4PeAt + 64 * n + 16 * t), q.pe[n], s[tb]);
             }
+        }
+        unpack(0);
+        if (!idle) {
             if (k0 + kTile > all_see) {
 #pragma unroll
                 for (int tb = 0; tb < kTB; ++tb)
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (k0 + 16 * (kw * kTB + tb) + 4 * t + x >= limit[nb]) s[tb][nb][x] = -INFINITY;
+                    for (int x = 0; x < 4; ++x)
+                        if (k0 + 16 * (kw * kTB + tb) + 4 * t + x >= limit) s[tb][x] = -INFINITY;
             }
-            bool move = false;
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                float y = s[0][nb][0];
+            for (int tb = 0; tb < kTB; ++tb)
 #pragma unroll
-                for (int tb = 0; tb < kTB; ++tb)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) y = fmaxf(y, s[tb][nb][x]);
-                top[nb] = max_over_quarters(y);
-                move |= (top[nb] - m[nb]) * c > 8.f || (m[nb] == -INFINITY && top[nb] > m[nb]);
-                before[nb] = lsum[nb];
-            }
+                for (int x = 0; x < 4; ++x) top = fmaxf(top, s[tb][x]);
+            top = max_over_quarters(top);
+            before = lsum;
             // the reference moves only when a row outgrows it by 2^8: the
             // probabilities go out against the one that stands, and again where it moves
             store_p();
-            if (__any(move) && l == 0) lds.moved[flag] = 1;
+            if (__any((top - m) * c > 8.f || (m == -INFINITY && top > m)) && l == 0) lds.moved[flag] = 1;
         }
         if (threadIdx.x == 0) lds.moved[flag == 2 ? 0 : flag + 1] = 0;
-        if constexpr (kRW > 1) wait_vm<(kBuf - 3) * kDma>();   // this wave's part of the next tile
+        wait_vm<(kBuf - 3) * kQ4Fetch>();   // this wave's part of the next tile
         raw_barrier();
-        if (__builtin_amdgcn_readfirstlane(lds.moved[flag])) {
+        const int moved = lds.moved[flag];
+        // the tile before is read: its memory takes the next one
+        issue(t0 + i + kBuf - 1, (i + kBuf - 1) % kBuf);
+        if (__builtin_amdgcn_readfirstlane(moved)) {
             if constexpr (kKW > 1) {
-                if (t == 0) {
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) lds.top[w][16 * nb + c16] = top[nb];
-                }
+                if (t == 0) lds.top[w][c16] = top;
                 raw_barrier();
             }
             if (!idle) {
+                float mn = fmaxf(m, top);
+                if constexpr (kKW > 1) {
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    float mn = fmaxf(m[nb], top[nb]);
-                    if constexpr (kKW > 1) {
-#pragma unroll
-                        for (int k = 0; k < kKW; ++k) mn = fmaxf(mn, lds.top[k * kRW + rw][16 * nb + c16]);
-                    }
-                    const float mun = mn == -INFINITY ? 0.f : mn * c;
-                    const float a = m[nb] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu[nb] - mun);
-                    m[nb] = mn;
-                    mu[nb] = mun;
-                    lsum[nb] = before[nb] * a;
-                    if (kw == 0 && t == 0) lds.factor[32 * rw + 16 * nb + c16] = a;
+                    for (int k = 0; k < kKW; ++k) mn = fmaxf(mn, lds.top[k * kRowWaves + rw][c16]);
                 }
+                const float mun = mn == -INFINITY ? 0.f : mn * c;
+                const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
+                m = mn;
+                mu = mun;
+                lsum = before * a;
+                if (kw == 0 && t == 0) lds.factor[16 * rw + c16] = a;
                 store_p();
             }
             raw_barrier();
@@ -363,29 +323,14 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
             for (int rb = 0; rb < kRW; ++rb) {
                 const float f = lds.factor[32 * rb + c32];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) acc[rb][b][x] *= f;
             }
         }
-        // the tile before is read: its memory takes the next one
-        issue(t0 + i + kBuf - 1, (i + kBuf - 1) % kBuf);
 #pragma unroll
         for (int ch = 0; ch < kTile / kValRows; ++ch) {
-            // this wave's 128 channels of 32 rows as bf16
-            const uint32_t row = tile + drow + ch * kValRows * kQ4Row;
-            const uint32_t sc = lds_read4(row + kQ4ScaleAt + 4 * w);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const u32x4 x = lds_read_u4(row + 64 * w + 32 * n + 16 * g);
-                const uint32_t sb = (sc >> (16 * n + 8 * g)) & 255;
-                // NaN groups are left out here: they have made the scores of all
-                // who see them NaN, and no others may meet them as 0 x NaN
-                const float f = q4_scale(sb == kQ4Bad ? 0 : sb);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    lds_write_u4(val + c32 * 256 + 16 * ((4 * (2 * n + g) + j) ^ val_swz(c32)), q4_eight(x[j], f));
-            }
+            if (ch > 0) unpack(ch);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 bf16x8 pr[kRW];
@@ -393,9 +338,9 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
                 for (int rb = 0; rb < kRW; ++rb)
                     pr[rb] = __builtin_bit_cast(bf16x8, lds.p[i & 1][rb][2 * ch + kk][l]);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const u32x2 x = lds_read_tr8((va[0] ^ (64 * b)) + kk * 16 * 256);
-                    const u32x2 y = lds_read_tr8((va[1] ^ (64 * b)) + kk * 16 * 256);
+                for (int b = 0; b < 2; ++b) {
+                    const u32x2 x = lds_read_tr8((vget[0] ^ (64 * b)) + kk * 16 * kValRow);
+                    const u32x2 y = lds_read_tr8((vget[1] ^ (64 * b)) + kk * 16 * kValRow);
                     const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
 #pragma unroll
                     for (int rb = 0; rb < kRW; ++rb)
@@ -404,46 +349,41 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
             }
         }
     }
-    (void)row_blocks;
     wait_vm<0>();   // the tiles behind the last: nothing may land later
-#pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-        const float y = sum_over_quarters(lsum[nb]);
-        if (t == 0) {
-            lds.l[w][16 * nb + c16] = y;
-            if (kw == 0) lds.mu[32 * rw + 16 * nb + c16] = m[nb] == -INFINITY ? -INFINITY : mu[nb];
-        }
+    lsum = sum_over_quarters(lsum);
+    if (t == 0) {
+        lds.l[w][c16] = lsum;
+        if (kw == 0) lds.mu[16 * rw + c16] = m == -INFINITY ? -INFINITY : mu;
     }
     raw_barrier();
 #pragma unroll
     for (int rb = 0; rb < kRW; ++rb) {
         float total = 0.f;
 #pragma unroll
-        for (int k = 0; k < kKW; ++k) total += lds.l[k * kRW + rb][c32];
+        for (int k = 0; k < kKW; ++k) total += lds.l[k * kRowWaves + 2 * rb + (c32 >> 4)][c16];
         const int lr = 32 * rb + c32;
-        if (w == rb % 4 && g == 0 && lr < sink.rows) {
+        if (w == rb && g == 0 && lr < sink.rows) {
             const float x = lds.mu[lr];
             if (!sink.final) *reinterpret_cast<f32x2*>(sink.ml + 2 * lr) = f32x2{x, total};
             else if (A.lse) A.lse[sink.row0 + lr] = total == 0.f ? -INFINITY : fmaf(x, kLn2, logf(total));
         }
         const float inv = !sink.final ? 1.f : total == 0.f ? 0.f : 1.f / total;
-        // 64 channels at a time by way of LDS, so that they leave row by row
+        // 32 channels at a time by way of LDS, so that they leave row by row
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int x = 0; x < 4; ++x) {
+                const f32x16& a = acc[rb][b];
+                const f32x4 y = {a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv, a[4 * x + 3] * inv};
+                lds_write_u4(vput + 16 * ((2 * x + g) ^ (c32 >> 1 & 7)), __builtin_bit_cast(u32x4, y));
+            }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const f32x16& a = acc[rb][2 * h + b];
-                    const f32x4 y = {a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv, a[4 * x + 3] * inv};
-                    lds_write_u4(val + c32 * 256 + 16 * ((8 * b + 2 * x + g) ^ c16), __builtin_bit_cast(u32x4, y));
-                }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int r = 4 * x + t, row = 32 * rb + r;
-                const f32x4 y = __builtin_bit_cast(f32x4, lds_read_u4(val + r * 256 + 16 * (c16 ^ (r & 15))));
+            for (int x = 0; x < 4; ++x) {
+                const int r = 8 * x + (l >> 3), row = 32 * rb + r;
+                const f32x4 y = __builtin_bit_cast(
+                    f32x4, lds_read_u4(val + r * kValRow + 16 * ((l & 7) ^ (r >> 1 & 7))));
                 if (row >= sink.rows) continue;
-                const int ch = 128 * w + 64 * h + 4 * c16;
+                const int ch = kValChannels * w + 32 * b + 4 * (l & 7);
                 if (sink.final)
                     *reinterpret_cast<u32x2*>(A.o + (sink.row0 + row) * kMlaLatent + ch) =
                         u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
@@ -458,7 +398,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 template <int kRW>
-__global__ __launch_bounds__(kThreads, 1) void mla_decode_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
     const int l = threadIdx.x & 63, w = wave_id(), wg = blockIdx.x;
 
@@ -475,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_q4_kernel(const MlaDec
         before = s - x;
         int total = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kWaves; ++k) {
             if (k < w) before += lds.scan[k];
             total += lds.scan[k];
         }
@@ -501,10 +441,11 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_q4_kernel(const MlaDec
         int most = n0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-        if (l == 0) lds.scan[4 + w] = most;
+        if (l == 0) lds.scan[kWaves + w] = most;
         __syncthreads();
-        most = __builtin_amdgcn_readfirstlane(
-            max(max(lds.scan[4], lds.scan[5]), max(lds.scan[6], lds.scan[7])));
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
+        most = __builtin_amdgcn_readfirstlane(most);
         int each = max(A.min_tiles, total / (kMlaWorkgroups - units / 2) + 1);
         for (int tries = 0; tries < 2 && !apart && each <= max(share, A.min_tiles) + kPieceTiles; ++tries) {
             if (most <= each + 1) each = most;
@@ -576,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 1) void mla_decode_q4_kernel(const MlaDec
 
 // The prefix: every block of 32 kRW query rows walks all prefix rows.
 template <int kRW>
-__global__ __launch_bounds__(kThreads, 1) void mla_prefix_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(kThreads, 2) void mla_prefix_q4_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
     const int wg = blockIdx.x;
     const int rows = A.batch * A.tokens * A.heads;
@@ -603,10 +544,10 @@ __global__ __launch_bounds__(kThreads, 1) void mla_prefix_q4_kernel(const MlaDec
 }
 
 // Joins the partial sums of a query row, a wave per row (eight channels a lane).
-__global__ __launch_bounds__(kThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
     const int l = threadIdx.x & 63;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
-    const int row = blockIdx.x * (kThreads / 64) + wave_id();
+    const int row = blockIdx.x * (kJoinThreads / 64) + wave_id();
     if (row >= A.batch * unit_rows) return;
     const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
     const int stride = 32 * A.row_waves;
@@ -702,7 +643,7 @@ hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
     else launch_private<1>(A, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int rows = A.batch * A.tokens * A.heads;
-    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kThreads), 0, stream>>>(A);
+    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 

@@ -41,4 +41,27 @@ __device__ __forceinline__ u32x4 q4_eight(uint32_t x, float scale) {
                  q4_pair<3>(x, scale)};
 }
 
+// Eight rows (of one page, so they lie one behind the other) into LDS as they
+// lie: four transfers, 200 granules of 16 bytes.  Rows from `valid` on are read
+// as zeros.
+constexpr int kQ4Fetch = 4;
+__device__ const __attribute__((aligned(16))) uint32_t kQ4Zeros[4] = {};
+
+__device__ __forceinline__ void q4_fetch_rows(const char* rows, int valid, uint32_t lds, int lane) {
+    const int l = here(lane);
+    if (valid >= 8) {
+#pragma unroll
+        for (int i = 0; i < kQ4Fetch - 1; ++i) dma16_at(rows, 16 * l + 1024 * i, lds + 1024 * i);
+        if (l < 8) dma16_at(rows, 16 * l + 1024 * 3, lds + 1024 * 3);
+    } else {
+        const char* const zeros = reinterpret_cast<const char*>(kQ4Zeros);
+#pragma unroll
+        for (int i = 0; i < kQ4Fetch; ++i) {
+            const int g = 64 * i + l, row = g * 5243 >> 17;   // g / 25
+            if (i < kQ4Fetch - 1 || l < 8)
+                dma16_from(row < valid ? rows + 16 * g : zeros, lds + 1024 * i);
+        }
+    }
+}
+
 }  // namespace rda
