@@ -95,12 +95,12 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // sums (64 KiB per 32 rows) than in tiles (36 KiB each).  2 instead of 4: 8 x
 // 270 rows x 80 query rows 26 us for 28, but 7 sequences of 950 rows 22.5 for
 // 20.5 and one of 777 rows 21 for 20.
-// tile: cached rows per tile of the kernel.
-size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, int32_t tile = 32) {
+size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
-    A.row_waves = unit_rows > 64 ? 4 : unit_rows > 32 ? 2 : 1;
+    const int most_waves = q4 ? 2 : 4, workgroups = q4 ? kQ4Workgroups : kMlaWorkgroups;
+    A.row_waves = unit_rows > 64 ? most_waves : unit_rows > 32 ? 2 : 1;
     A.row_blocks = int32_t((unit_rows + 32 * A.row_waves - 1) / (32 * A.row_waves));
-    A.min_tiles = 128 / tile;   // (and no more than an average unit has: see the kernel)
+    A.min_tiles = 4;   // (and no more than an average unit has: see the kernel)
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* p = ws ? ws + at : nullptr;
@@ -109,8 +109,8 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, int32_t tile = 32) {
     };
     const size_t units = size_t(A.batch) * A.row_blocks;
     A.meta = reinterpret_cast<int32_t*>(take(units * 2 * sizeof(int32_t)));
-    A.bad = reinterpret_cast<int32_t*>(take((units + kMlaWorkgroups) * sizeof(int32_t)));
-    const size_t slots = (units + kMlaWorkgroups) * 32 * A.row_waves;
+    A.bad = reinterpret_cast<int32_t*>(take((units + workgroups) * sizeof(int32_t)));
+    const size_t slots = (units + workgroups) * 32 * A.row_waves;
     A.part = reinterpret_cast<float*>(take(slots * RDA_MLA_LATENT * sizeof(float)));
     A.part_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
     A.prefix_waves = 1;
@@ -120,31 +120,30 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, int32_t tile = 32) {
         // blocks of 128 rows once they fill the chip with long shares, or half of it
         // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
         // blocks of 32, whose four waves share out the tiles
-        const int64_t tiles = (int64_t(A.prefix_len) + tile - 1) / tile;
-        const int64_t blocks = (rows + 127) / 128;
-        A.prefix_waves =
-            blocks * tiles * tile >= 256 * kMlaWorkgroups || 2 * blocks >= kMlaWorkgroups ? 4 : 1;
+        const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
+        const int64_t blocks = (rows + 32 * most_waves - 1) / (32 * most_waves);
+        A.prefix_waves = blocks * tiles >= 8 * workgroups || 2 * blocks >= workgroups ? most_waves : 1;
         A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
-        const int64_t share = (A.prefix_units * tiles + kMlaWorkgroups - 1) / kMlaWorkgroups;
-        const int64_t least = tiles < 256 / tile ? tiles : 256 / tile;   // (no more than a block has)
+        const int64_t share = (A.prefix_units * tiles + workgroups - 1) / workgroups;
+        const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
         A.prefix_per = int32_t(share > least ? share : least);
         A.pre_bad = reinterpret_cast<int32_t*>(
-            take((size_t(A.prefix_units) + kMlaWorkgroups) * sizeof(int32_t)));
-        const size_t ps = (size_t(A.prefix_units) + kMlaWorkgroups) * 32 * A.prefix_waves;
+            take((size_t(A.prefix_units) + workgroups) * sizeof(int32_t)));
+        const size_t ps = (size_t(A.prefix_units) + workgroups) * 32 * A.prefix_waves;
         A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));
     }
     return at;
 }
 
-size_t mla_decode_bytes(int32_t batch, int32_t tokens, int32_t num_heads, int32_t prefix_len, int32_t tile) {
+size_t mla_decode_bytes(int32_t batch, int32_t tokens, int32_t num_heads, int32_t prefix_len, bool q4) {
     MlaDecodeArgs A{};
     if (check_mla_decode_sizes(batch, tokens, num_heads, prefix_len) != RDA_OK) return 0;
     A.batch = batch;
     A.tokens = tokens;
     A.heads = num_heads;
     A.prefix_len = prefix_len;
-    return mla_decode_plan(A, nullptr, tile);
+    return mla_decode_plan(A, nullptr, q4);
 }
 
 // rda_mla_decode and, with q4, rda_mla_decode_q4 (page_stride in bytes).
@@ -183,11 +182,10 @@ rda_status mla_decode_any(bool q4, const void* q, const void* cache, int64_t pag
     A.tokens = tokens;
     A.heads = num_heads;
     A.prefix_len = prefix_len;
-    const int32_t tile = q4 ? 64 : 32;
-    const size_t need = mla_decode_plan(A, nullptr, tile);
+    const size_t need = mla_decode_plan(A, nullptr, q4);
     if (!workspace || workspace_bytes < need) return RDA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return RDA_ERR_ALIGN;
-    mla_decode_plan(A, static_cast<unsigned char*>(workspace), tile);
+    mla_decode_plan(A, static_cast<unsigned char*>(workspace), q4);
     const size_t rows = size_t(batch) * tokens * num_heads;
     const Range in[] = {rng(q, rows * RDA_MLA_ROW * 2),
                         q4 ? q4_range(cache, page_stride, num_pages, page_tokens)
@@ -1259,7 +1257,7 @@ rda_status rda_mla_prefill(const void* q, int64_t q_stride, const void* kv, int6
 
 size_t rda_mla_decode_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
                                       int32_t prefix_len) {
-    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, 32);
+    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, false);
 }
 
 rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
@@ -1274,7 +1272,7 @@ rda_status rda_mla_decode(const void* q, const void* cache, int64_t page_stride,
 
 size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t num_heads,
                                          int32_t prefix_len) {
-    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, 64);
+    return mla_decode_bytes(batch, tokens, num_heads, prefix_len, true);
 }
 
 rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,

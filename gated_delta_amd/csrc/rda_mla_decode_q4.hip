@@ -7,27 +7,26 @@
 namespace rda {
 namespace {
 
-typedef const __attribute__((address_space(4))) int32_t const_i32;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kJoinThreads = 256;
-constexpr int kTile = 64;                        // cached rows per tile
-constexpr int kTileBytes = kTile * kQ4Row;       // 25600
+constexpr int kTile = 32;                        // cached rows per tile
+constexpr int kTileBytes = kTile * kQ4Row;       // 12800
 constexpr int kWaveRows = kTile / kWaves;        // rows of a tile that a wave fetches
 constexpr int kWaveBytes = kWaveRows * kQ4Row;
-constexpr int kValRows = 32;                     // rows unpacked at a time
+constexpr int kBuf = 4;                          // tiles in flight or in use
+constexpr int kValRows = 16;                     // rows unpacked at a time
 constexpr int kValChannels = kMlaLatent / kWaves;
+constexpr int kBlocks = kValChannels / 32;       // blocks of 32 channels a wave sums
 constexpr int kValRow = kValChannels * 2;        // bytes
 constexpr int kValBytes = kValRows * kValRow;
-constexpr int kPieceTiles = 3;
+constexpr int kPieceTiles = 6;
 
 template <int kRW>
 struct Lds {
-    static constexpr int kBuf = kRW == 4 ? 3 : 4;   // tiles in flight or in use
     unsigned char tile[kBuf][kTileBytes];
     unsigned char val[kWaves][kValBytes];   // a wave's own: unpacked values of its channels
     u32x4 p[2][kRW][kTile / 16][64];        // probabilities: [32 query rows][16 cached rows][lane]
@@ -75,14 +74,20 @@ __device__ __forceinline__ uint32_t lds_read4(uint32_t a) {
 __device__ __forceinline__ u32x4 lds_read_u4(uint32_t a) {
     return *(const lds_u32x4*)(lds_char*)uintptr_t(a);
 }
+__device__ __forceinline__ void lds_write_u2(uint32_t a, u32x2 x) {
+    typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+    *(lds_u32x2*)(lds_char*)uintptr_t(a) = x;
+}
 __device__ __forceinline__ void lds_write_u4(uint32_t a, u32x4 x) {
     *(lds_u32x4*)(lds_char*)uintptr_t(a) = x;
 }
 
-// Row r of unpacked values (128 bytes) keeps 16-byte granule j at j ^ val_swz(r):
-// sixteen rows written at one granule, and the rows and granules that a
+// Row r of unpacked values (256 bytes) keeps 16-byte granule j at j ^ val_swz(r):
+// eight rows written at one granule, and the rows and granules that a
 // transposing read touches at a time, fall on distinct banks.
-__device__ __forceinline__ int val_swz(int r) { return (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1 | (r >> 2 & 1); }
+__device__ __forceinline__ int val_swz(int r) {
+    return (r >> 1 & 1) * 10 | (r & 1) << 2 | (r >> 2 & 1);
+}
 
 __device__ __forceinline__ int clamp_len(const MlaDecodeArgs& A, int b) {
     const int64_t most = int64_t(A.table_width) << A.page_shift;
@@ -94,11 +99,6 @@ struct Source {
     const int32_t* table;
     int len;
 };
-
-__device__ __forceinline__ int page_of(const MlaDecodeArgs& A, const Source& src, int k) {
-    const int at = k < src.len ? k >> A.page_shift : 0;
-    return src.len > 0 ? min(max(((const_i32*)src.table)[at], 0), A.num_pages - 1) : 0;
-}
 
 // Where a piece's sums go: the outputs, or a slot of partial sums.
 struct Sink {
@@ -170,7 +170,6 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
                                       int t1, const Sink& sink) {
     constexpr int kRowWaves = 2 * kRW, kKW = kWaves / kRowWaves;   // row waves, key waves
     constexpr int kTB = kTile / 16 / kKW;                          // blocks of 16 cached rows a wave scores
-    constexpr int kBuf = Lds<kRW>::kBuf;
     const int w = wave_id(), l = threadIdx.x & 63;
     const int rw = w % kRowWaves, kw = w / kRowWaves;
     const int c16 = l & 15, t = l >> 4, c32 = l & 31, g = l >> 5;
@@ -180,15 +179,25 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     const uint32_t tiles = lds_addr(&lds.tile[0][0]);
     const uint32_t val = lds_addr(&lds.val[w][0]);
 
-    int page;   // of this wave's rows of the next tile to fetch
+    // lane j: the page of this wave's rows of tile `pages_from` + j
+    int pages, pages_from = t0;
+    auto load_pages = [&]() {
+        const int k = (pages_from + l) * kTile + kWaveRows * w;
+        pages = src.len > 0 ? src.table[k < src.len ? k >> A.page_shift : 0] : 0;
+        pages = min(max(pages, 0), A.num_pages - 1);
+    };
+    load_pages();
     auto issue = [&](int tile, int buf) {
+        if (tile - pages_from == 64) {
+            pages_from = tile;
+            load_pages();
+        }
         const int k = tile * kTile + kWaveRows * w;
+        const int page = __builtin_amdgcn_readlane(pages, tile - pages_from);
         q4_fetch_rows(reinterpret_cast<const char*>(A.cache) + int64_t(page) * A.page_stride +
                           int64_t(k & ((1 << A.page_shift) - 1)) * kQ4Row,
                       end - k, tiles + buf * kTileBytes + w * kWaveBytes, l);
-        page = page_of(A, src, k + kTile);
     };
-    page = page_of(A, src, t0 * kTile + kWaveRows * w);
 #pragma unroll 1
     for (int d = 0; d < kBuf - 1; ++d) issue(t0 + d, d);
 
@@ -197,20 +206,19 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     const int qrow = min(16 * rw + c16, sink.rows - 1);
     load_query(q, A.q + (sink.row0 + qrow) * kMlaRow, t);
     const int limit = kCausal ? src.len - (A.tokens - 1 - (sink.first_row + qrow) / A.heads) : src.len;
-    f32x16 acc[kRW][2];
+    f32x16 acc[kRW][kBlocks];
 #pragma unroll
     for (int rb = 0; rb < kRW; ++rb)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[rb][b][i] = 0.f;
 
     // this lane's addresses, from a tile's start
     const uint32_t krow = (kw * kTB * 16 + c16) * kQ4Row;                // the row it scores
-    const uint32_t drow = c32 * kQ4Row + kQ4ScaleAt / kWaves * w + 16 * g;   // its part of the row it unpacks
-    const uint32_t dscale = c32 * kQ4Row + kQ4ScaleAt + (2 * w & ~3);
-    const int dshift = 8 * ((2 * w & 3) + g);
-    const uint32_t vput = val + c32 * kValRow;
+    const uint32_t drow = c16 * kQ4Row + kQ4ScaleAt / kWaves * w + 16 * t;   // its part of the row it unpacks
+    const uint32_t dscale = c16 * kQ4Row + kQ4ScaleAt + 4 * w;
+    const uint32_t vput = val + c16 * kValRow;
     const int vr = 8 * g + (c16 >> 2), vlow = 2 * (t & 1) + ((c16 >> 1) & 1);
     uint32_t vget[2];
 #pragma unroll
@@ -221,23 +229,49 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
 
     wait_vm<(kBuf - 2) * kQ4Fetch>();
     raw_barrier();
+    f32x4 s[kTB];
+    // this wave's scores of the tile at `tile`
+    auto scores = [&](uint32_t tile) {
+#pragma unroll
+        for (int tb = 0; tb < kTB; ++tb) {
+            const uint32_t row = tile + krow + tb * 16 * kQ4Row;
+            const int sc = int(lds_read4(row + kQ4ScaleAt + 4 * t));
+            f32x4 hi = zero4(), lo = zero4();   // (two chains: each product waits for the one before)
+            each<4>([&](auto mm) {
+                constexpr int n = decltype(mm)::value;
+                const u32x4 k4 = lds_read_u4(row + 64 * t + 16 * n);
+                const i32x8 a = {int(k4[0]), int(k4[1]), int(k4[2]), int(k4[3]), 0, 0, 0, 0};
+                hi = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.hi[n], hi, 4, 0, n, sc, 0, int(q.scale));
+                lo = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.lo[n], lo, 4, 0, n, sc, 1, int(q.scale));
+            });
+            hi = mfma_bf16(lds_read16(row + kQ4PeAt + 16 * t), q.pe[0], hi);
+            lo = mfma_bf16(lds_read16(row + kQ4PeAt + 64 + 16 * t), q.pe[1], lo);
+            s[tb] = hi + lo;
+        }
+    };
+    if (!idle) scores(tiles);
     const int n_tiles = t1 - t0;
     for (int i = 0; i < n_tiles; ++i) {
         const int k0 = (t0 + i) * kTile, buf = i % kBuf, flag = i % 3;
         const uint32_t tile = tiles + buf * kTileBytes;
-        // 32 rows of this wave's 64 channels as bf16
-        auto unpack = [&](int ch) {
+        const uint32_t pbuf = (i & 1) * sizeof(lds.p[0]);
+        // 16 rows of this wave's 128 channels: a lane unpacks a group of a row
+        u32x4 codes[kTile / kValRows];
+        float unit[kTile / kValRows];
+#pragma unroll
+        for (int ch = 0; ch < kTile / kValRows; ++ch) {
             const uint32_t at = tile + ch * kValRows * kQ4Row;
-            const uint32_t sb = (lds_read4(at + dscale) >> dshift) & 255;
-            const u32x4 x = lds_read_u4(at + drow);
+            const uint32_t sb = (lds_read4(at + dscale) >> (8 * t)) & 255;
+            codes[ch] = lds_read_u4(at + drow);
             // NaN groups are left out here: they have made the scores of all who
             // see them NaN, and no others may meet them as 0 x NaN
-            const float f = q4_scale(sb == kQ4Bad ? 0 : sb);
+            unit[ch] = q4_scale(sb == kQ4Bad ? 0 : sb);
+        }
+        auto unpack = [&](int ch) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                lds_write_u4(vput + 16 * ((4 * g + j) ^ val_swz(c32)), q4_eight(x[j], f));
+                lds_write_u4(vput + 16 * ((4 * t + j) ^ val_swz(c16)), q4_eight(codes[ch][j], unit[ch]));
         };
-        f32x4 s[kTB];
         auto store_p = [&]() {
 #pragma unroll
             for (int tb = 0; tb < kTB; ++tb) {
@@ -247,33 +281,11 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
                     e[x] = __builtin_amdgcn_exp2f(fmaf(s[tb][x], c, -mu));
                     lsum += e[x];
                 }
-                typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
-                *(lds_u32x2*)(lds_char*)uintptr_t(pput + (i & 1) * sizeof(lds.p[0]) + tb * sizeof(lds.p[0][0][0])) =
-                    u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])};
+                lds_write_u2(pput + pbuf + tb * sizeof(lds.p[0][0][0]),
+                             u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])});
             }
         };
         float top = -INFINITY, before = 0.f;
-        if (!idle) {
-#pragma unroll
-            for (int tb = 0; tb < kTB; ++tb) {
-                const uint32_t row = tile + krow + tb * 16 * kQ4Row;
-                const int sc = int(lds_read4(row + kQ4ScaleAt + 4 * t));
-                s[tb] = zero4();
-                each<4>([&](auto mm) {
-                    constexpr int n = decltype(mm)::value;
-                    const u32x4 k4 = lds_read_u4(row + 64 * t + 16 * n);
-                    const i32x8 a = {int(k4[0]), int(k4[1]), int(k4[2]), int(k4[3]), 0, 0, 0, 0};
-                    s[tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.hi[n], s[tb], 4, 0, n, sc, 0,
-                                                                            int(q.scale));
-                    s[tb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.lo[n], s[tb], 4, 0, n, sc, 1,
-                                                                            int(q.scale));
-                });
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    s[tb] = mfma_bf16(lds_read16(row + kQ4PeAt + 64 * n + 16 * t), q.pe[n], s[tb]);
-            }
-        }
-        unpack(0);
         if (!idle) {
             if (k0 + kTile > all_see) {
 #pragma unroll
@@ -294,6 +306,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
             if (__any((top - m) * c > 8.f || (m == -INFINITY && top > m)) && l == 0) lds.moved[flag] = 1;
         }
         if (threadIdx.x == 0) lds.moved[flag == 2 ? 0 : flag + 1] = 0;
+        unpack(0);
         wait_vm<(kBuf - 3) * kQ4Fetch>();   // this wave's part of the next tile
         raw_barrier();
         const int moved = lds.moved[flag];
@@ -323,29 +336,28 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
             for (int rb = 0; rb < kRW; ++rb) {
                 const float f = lds.factor[32 * rb + c32];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) acc[rb][b][x] *= f;
             }
         }
+        // the scores of the next tile (zeros behind the last) beside this one's sums
+        const uint32_t next = tiles + (buf + 1 == kBuf ? 0 : buf + 1) * kTileBytes;
+        if (!idle) scores(next);
 #pragma unroll
         for (int ch = 0; ch < kTile / kValRows; ++ch) {
             if (ch > 0) unpack(ch);
+            bf16x8 pr[kRW];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 pr[kRW];
+            for (int rb = 0; rb < kRW; ++rb) pr[rb] = __builtin_bit_cast(bf16x8, lds.p[i & 1][rb][ch][l]);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const u32x2 x = lds_read_tr8(vget[0] ^ (64 * b));
+                const u32x2 y = lds_read_tr8(vget[1] ^ (64 * b));
+                const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
 #pragma unroll
                 for (int rb = 0; rb < kRW; ++rb)
-                    pr[rb] = __builtin_bit_cast(bf16x8, lds.p[i & 1][rb][2 * ch + kk][l]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const u32x2 x = lds_read_tr8((vget[0] ^ (64 * b)) + kk * 16 * kValRow);
-                    const u32x2 y = lds_read_tr8((vget[1] ^ (64 * b)) + kk * 16 * kValRow);
-                    const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
-#pragma unroll
-                    for (int rb = 0; rb < kRW; ++rb)
-                        acc[rb][b] = mfma32(v, pr[rb], acc[rb][b]);
-                }
+                    acc[rb][b] = mfma32(v, pr[rb], acc[rb][b]);
             }
         }
     }
@@ -370,18 +382,18 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
         const float inv = !sink.final ? 1.f : total == 0.f ? 0.f : 1.f / total;
         // 32 channels at a time by way of LDS, so that they leave row by row
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const f32x16& a = acc[rb][b];
                 const f32x4 y = {a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv, a[4 * x + 3] * inv};
-                lds_write_u4(vput + 16 * ((2 * x + g) ^ (c32 >> 1 & 7)), __builtin_bit_cast(u32x4, y));
+                lds_write_u4(val + c32 * 128 + 16 * ((2 * x + g) ^ (c32 & 7)), __builtin_bit_cast(u32x4, y));
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int r = 8 * x + (l >> 3), row = 32 * rb + r;
                 const f32x4 y = __builtin_bit_cast(
-                    f32x4, lds_read_u4(val + r * kValRow + 16 * ((l & 7) ^ (r >> 1 & 7))));
+                    f32x4, lds_read_u4(val + r * 128 + 16 * ((l & 7) ^ (r & 7))));
                 if (row >= sink.rows) continue;
                 const int ch = kValChannels * w + 32 * b + 4 * (l & 7);
                 if (sink.final)
@@ -433,11 +445,11 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
     }
     total *= A.row_blocks;
     if (total == 0) return;
-    const int share = (total + kMlaWorkgroups - 1) / kMlaWorkgroups;
+    const int share = (total + kQ4Workgroups - 1) / kQ4Workgroups;
     const int units = A.batch * A.row_blocks;
     int per = max(share, min(A.min_tiles, (total + units - 1) / units));
     bool apart = false;
-    if (units <= kMlaWorkgroups && share < 1 << 20) {
+    if (units <= kQ4Workgroups && A.batch <= kThreads && share < 1 << 20) {
         int most = n0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
@@ -446,13 +458,13 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
         most = __builtin_amdgcn_readfirstlane(most);
-        int each = max(A.min_tiles, total / (kMlaWorkgroups - units / 2) + 1);
+        int each = max(A.min_tiles, total / (kQ4Workgroups - units / 2) + 1);
         for (int tries = 0; tries < 2 && !apart && each <= max(share, A.min_tiles) + kPieceTiles; ++tries) {
-            if (most <= each + 1) each = most;
+            if (most <= each + 2) each = most;
             const int padded = (n0 + each - 1) / each * each;
             int before;
             const int sum = block_sum(padded, before);
-            if (sum * A.row_blocks <= each * kMlaWorkgroups) {
+            if (sum * A.row_blocks <= each * kQ4Workgroups) {
                 apart = true;
                 per = each;
                 n0 = padded;
@@ -544,10 +556,10 @@ __global__ __launch_bounds__(kThreads, 2) void mla_prefix_q4_kernel(const MlaDec
 }
 
 // Joins the partial sums of a query row, a wave per row (eight channels a lane).
-__global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(kThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
     const int l = threadIdx.x & 63;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
-    const int row = blockIdx.x * (kJoinThreads / 64) + wave_id();
+    const int row = blockIdx.x * (kThreads / 64) + wave_id();
     if (row >= A.batch * unit_rows) return;
     const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
     const int stride = 32 * A.row_waves;
@@ -620,7 +632,7 @@ __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDeco
 
 template <int kRW>
 void launch_private(const MlaDecodeArgs& A, hipStream_t stream) {
-    mla_decode_q4_kernel<kRW><<<dim3(kMlaWorkgroups), dim3(kThreads), 0, stream>>>(A);
+    mla_decode_q4_kernel<kRW><<<dim3(kQ4Workgroups), dim3(kThreads), 0, stream>>>(A);
 }
 
 template <int kRW>
@@ -634,16 +646,15 @@ void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
 
 hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
     if (A.prefix_len) {
-        if (A.prefix_waves == 4) launch_prefix<4>(A, stream);
+        if (A.prefix_waves == 2) launch_prefix<2>(A, stream);
         else launch_prefix<1>(A, stream);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (A.row_waves == 4) launch_private<4>(A, stream);
-    else if (A.row_waves == 2) launch_private<2>(A, stream);
+    if (A.row_waves == 2) launch_private<2>(A, stream);
     else launch_private<1>(A, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int rows = A.batch * A.tokens * A.heads;
-    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
+    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
