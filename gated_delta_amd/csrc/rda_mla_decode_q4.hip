@@ -7,35 +7,39 @@
 namespace rda {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
-constexpr int kWaveRows = kTile / kWaves;        // rows of a tile that a wave fetches
-constexpr int kWaveBytes = kWaveRows * kQ4Row;
-constexpr int kBuf = 4;                          // tiles in flight or in use
-constexpr int kValRows = 16;                     // rows unpacked at a time
-constexpr int kValChannels = kMlaLatent / kWaves;
-constexpr int kBlocks = kValChannels / 32;       // blocks of 32 channels a wave sums
-constexpr int kValRow = kValChannels * 2;        // bytes
-constexpr int kValBytes = kValRows * kValRow;
+constexpr int kJoinThreads = 256;
 constexpr int kPieceTiles = 6;
+
+// A workgroup of 32 kRW query rows: 4 kRW waves.
+template <int kRW>
+struct Shape {
+    static constexpr int kWaves = 4 * kRW, kThreads = 64 * kWaves;
+    static constexpr int kRowWaves = 2 * kRW, kKeyWaves = 2;        // of 16 query rows, 16 cached rows each
+    static constexpr int kFetchRows = kTile / 4;                    // waves 0 .. 3 fetch a tile
+    static constexpr int kChannels = kMlaLatent / kWaves;           // that a wave sums
+    static constexpr int kBlocks = kChannels / 32;
+    static constexpr int kValRows = 16 * kRW;                       // rows that a wave unpacks at a time
+    static constexpr int kValRow = kChannels * 2, kValBytes = kValRows * kValRow;
+};
 
 template <int kRW>
 struct Lds {
-    unsigned char tile[kBuf][kTileBytes];
-    unsigned char val[kWaves][kValBytes];   // a wave's own: unpacked values of its channels
-    u32x4 p[2][kRW][kTile / 16][64];        // probabilities: [32 query rows][16 cached rows][lane]
-    float top[kWaves][16];
-    float l[kWaves][16];
+    static constexpr int kBuf = 4 * kRW;   // tiles in flight or in use
+    unsigned char tile[kBuf][kTileBytes];   // (the last two and what follows: queries on their way in)
+    unsigned char val[Shape<kRW>::kWaves][Shape<kRW>::kValBytes];   // a wave's own: unpacked values
+    u32x4 p[2][kRW][kTile / 16][64];   // probabilities: [32 query rows][16 cached rows][lane]
+    float top[Shape<kRW>::kWaves][16];
+    float l[Shape<kRW>::kWaves][16];
+    uint32_t qscale[kRW * 32];
     float mu[kRW * 32];
     float factor[kRW * 32];
-    int moved[3];
-    int scan[2 * kWaves];
+    int moved[2];
+    int scan[2 * Shape<kRW>::kWaves];
     int unit, first;
 };
 
@@ -82,11 +86,12 @@ __device__ __forceinline__ void lds_write_u4(uint32_t a, u32x4 x) {
     *(lds_u32x4*)(lds_char*)uintptr_t(a) = x;
 }
 
-// Row r of unpacked values (256 bytes) keeps 16-byte granule j at j ^ val_swz(r):
-// eight rows written at one granule, and the rows and granules that a
-// transposing read touches at a time, fall on distinct banks.
+// Row r of unpacked values (256 or 128 bytes) keeps 16-byte granule j at
+// j ^ val_swz(r): eight rows written at one granule, and the rows and granules
+// that a transposing read touches at a time, fall on distinct banks.
+template <int kRow>
 __device__ __forceinline__ int val_swz(int r) {
-    return (r >> 1 & 1) * 10 | (r & 1) << 2 | (r >> 2 & 1);
+    return (r >> 1 & 1) * (kRow == 256 ? 10 : 4) | (r & 1) * (kRow == 256 ? 4 : 2) | (r >> 2 & 1);
 }
 
 __device__ __forceinline__ int clamp_len(const MlaDecodeArgs& A, int b) {
@@ -117,302 +122,401 @@ struct Query {
     uint32_t scale;    // scale bytes of hi and lo
 };
 
-__device__ __forceinline__ void load_query(Query& Q, const uint16_t* row, int t) {
-    u32x4 x[4][4];   // [product][16 bytes]
+// Query rows as pairs of 8-bit values into LDS at `at` (hi, then lo: 512 bytes a
+// row, 16-byte granule j at j ^ (row & 15)) and their scale bytes into `scales`:
+// a wave a row, eight values a lane.
+template <int kRW>
+__device__ __forceinline__ void stage_query(const MlaDecodeArgs& A, const Sink& sink, uint32_t at, uint32_t* scales) {
+    typedef Shape<kRW> S;
+    constexpr int kRows = 32 * kRW / S::kWaves;   // of a wave: 8
+    const int w = wave_id(), l = here(threadIdx.x & 63);
+    u32x4 x[kRows];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int i = 0; i < kRows; ++i)
+        x[i] = *reinterpret_cast<const u32x4*>(
+            A.q + (sink.row0 + min(kRows * w + i, sink.rows - 1)) * kMlaRow + 8 * l);
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            x[m][h] = *reinterpret_cast<const u32x4*>(
-                row + 256 * (h >> 1) + 32 * (4 * (t >> 1) + m) + 16 * (t & 1) + 8 * (h & 1));
+    for (int i = 0; i < kRows; ++i) {
+        const int row = kRows * w + i;
+        u16x2 most = {};
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-        Q.pe[m] = __builtin_bit_cast(
-            bf16x8, *reinterpret_cast<const u32x4*>(row + kMlaLatent + 32 * m + 8 * t));
-    u16x2 most = {};
+        for (int d = 0; d < 4; ++d)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x[i][d] & 0x7fff7fffu));
+        const uint32_t e = umax_over_quarters(dpp_umax16(max(uint32_t(most[0]), uint32_t(most[1])))) >> 7;
+        // the largest value lands in [128, 256) of hi's scale
+        const uint32_t sh = max(int(e) - 7, 24), sl = sh - 5;
+        const float fh = q4_scale(sh), fl = q4_scale(sl);
+        uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x[m][h][i] & 0x7fff7fffu));
-    const uint32_t e = umax_over_quarters(max(uint32_t(most[0]), uint32_t(most[1]))) >> 7;
-    // the largest value lands in [128, 256) of hi's scale
-    const uint32_t sh = max(int(e) - 7, 24), sl = sh - 5;
-    Q.scale = e == 255 ? 0xffffu : sh | sl << 8;
-    const float fh = q4_scale(sh), fl = q4_scale(sl);
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {   // four values a dword
-                s16x2 hi = {}, lo = {};
-                const uint32_t a = x[m][h][2 * d], b = x[m][h][2 * d + 1];
-                hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(hi, __builtin_bit_cast(bf16x2, a), fh, false);
-                hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(hi, __builtin_bit_cast(bf16x2, b), fh, true);
-                const uint32_t hw = __builtin_bit_cast(uint32_t, hi);
-                const f32x2 ra = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hw, fh, false);
-                const f32x2 rb = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hw, fh, true);
-                lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
-                    lo, __uint_as_float(a << 16) - ra[0], __uint_as_float(a & 0xffff0000u) - ra[1], fl, false);
-                lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
-                    lo, __uint_as_float(b << 16) - rb[0], __uint_as_float(b & 0xffff0000u) - rb[1], fl, true);
-                Q.hi[m][2 * h + d] = int(hw);
-                Q.lo[m][2 * h + d] = __builtin_bit_cast(int, lo);
-            }
+        for (int d = 0; d < 2; ++d) {   // four values a dword
+            s16x2 y = {}, z = {};
+            const uint32_t a = x[i][2 * d], b = x[i][2 * d + 1];
+            y = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(y, __builtin_bit_cast(bf16x2, a), fh, false);
+            y = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(y, __builtin_bit_cast(bf16x2, b), fh, true);
+            hi[d] = __builtin_bit_cast(uint32_t, y);
+            const f32x2 ra = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[d], fh, false);
+            const f32x2 rb = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi[d], fh, true);
+            z = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
+                z, __uint_as_float(a << 16) - ra[0], __uint_as_float(a & 0xffff0000u) - ra[1], fl, false);
+            z = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
+                z, __uint_as_float(b << 16) - rb[0], __uint_as_float(b & 0xffff0000u) - rb[1], fl, true);
+            lo[d] = __builtin_bit_cast(uint32_t, z);
+        }
+        const uint32_t to = at + row * 512 + 16 * ((l >> 1) ^ (row & 15)) + 8 * (l & 1);
+        lds_write_u2(to, u32x2{hi[0], hi[1]});
+        lds_write_u2(to + 32 * kRW * 512, u32x2{lo[0], lo[1]});
+        if (l == 0) scales[row] = e == 255 ? 0xffffu : sh | sl << 8;
+    }
 }
+
+// Its 16 rows of them as a wave's operands.
+template <int kRW>
+__device__ __forceinline__ void take_query(Query& Q, uint32_t at, const uint32_t* scales, int row, int t) {
+    auto sixteen = [&](int part, int g) {   // 16 bytes
+        return lds_read_u4(at + (32 * kRW * part + row) * 512 + 16 * (g ^ (row & 15)));
+    };
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int g = 2 * (4 * (t >> 1) + m) + (t & 1);
+        const u32x4 a = sixteen(0, g), b = sixteen(0, g + 16), c = sixteen(1, g), d = sixteen(1, g + 16);
+        Q.hi[m] = i32x8{int(a[0]), int(a[1]), int(a[2]), int(a[3]), int(b[0]), int(b[1]), int(b[2]), int(b[3])};
+        Q.lo[m] = i32x8{int(c[0]), int(c[1]), int(c[2]), int(c[3]), int(d[0]), int(d[1]), int(d[2]), int(d[3])};
+    }
+    Q.scale = scales[row];
+}
+
+// The reference of a row that has seen no score.
+constexpr float kNone = -3e38f;
 
 // One piece: tiles [t0, t1) of a source for 32 kRW query rows.
 template <int kRW, bool kCausal>
 __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, const Source& src, int t0,
-                                      int t1, const Sink& sink) {
-    constexpr int kRowWaves = 2 * kRW, kKW = kWaves / kRowWaves;   // row waves, key waves
-    constexpr int kTB = kTile / 16 / kKW;                          // blocks of 16 cached rows a wave scores
+                                      int t1, const Sink& sink, int& turn) {
+    typedef Shape<kRW> S;
+    constexpr int kBuf = Lds<kRW>::kBuf, kBlocks = S::kBlocks, kValRow = S::kValRow;
     const int w = wave_id(), l = threadIdx.x & 63;
-    const int rw = w % kRowWaves, kw = w / kRowWaves;
+    const int rw = w % S::kRowWaves, kw = w / S::kRowWaves;
     const int c16 = l & 15, t = l >> 4, c32 = l & 31, g = l >> 5;
     const int end = min(src.len, t1 * kTile);
-    const int all_see = kCausal ? src.len - (A.tokens - 1) : src.len;
     const float c = A.scale * kLog2e;
     const uint32_t tiles = lds_addr(&lds.tile[0][0]);
     const uint32_t val = lds_addr(&lds.val[w][0]);
 
-    // lane j: the page of this wave's rows of tile `pages_from` + j
-    int pages, pages_from = t0;
-    auto load_pages = [&]() {
-        const int k = (pages_from + l) * kTile + kWaveRows * w;
-        pages = src.len > 0 ? src.table[k < src.len ? k >> A.page_shift : 0] : 0;
-        pages = min(max(pages, 0), A.num_pages - 1);
+    // lane j: where this wave's rows of tile rows_from + j lie
+    const char* rows = nullptr;
+    int rows_from = t0;
+    auto find_rows = [&]() {
+        const int k = (rows_from + l) * kTile + S::kFetchRows * w;
+        const int page = src.len > 0 ? src.table[k < src.len ? k >> A.page_shift : 0] : 0;
+        rows = reinterpret_cast<const char*>(A.cache) +
+               int64_t(min(max(page, 0), A.num_pages - 1)) * A.page_stride +
+               (k & ((1 << A.page_shift) - 1)) * kQ4Row;
     };
-    load_pages();
-    auto issue = [&](int tile, int buf) {
-        if (tile - pages_from == 64) {
-            pages_from = tile;
-            load_pages();
+    const uint32_t lane16 = 16 * l;
+    auto issue = [&](int tile) {
+        if (S::kWaves > 4 && w >= 4) return;
+        if (tile - rows_from == 64) {
+            rows_from = tile;
+            find_rows();
         }
-        const int k = tile * kTile + kWaveRows * w;
-        const int page = __builtin_amdgcn_readlane(pages, tile - pages_from);
-        q4_fetch_rows(reinterpret_cast<const char*>(A.cache) + int64_t(page) * A.page_stride +
-                          int64_t(k & ((1 << A.page_shift) - 1)) * kQ4Row,
-                      end - k, tiles + buf * kTileBytes + w * kWaveBytes, l);
+        const int j = tile - rows_from;
+        const uint64_t r = reinterpret_cast<uint64_t>(rows);
+        const char* const from = reinterpret_cast<const char*>(
+            uint64_t(uint32_t(__builtin_amdgcn_readlane(int(r >> 32), j))) << 32 |
+            uint32_t(__builtin_amdgcn_readlane(int(r), j)));
+        const int valid = end - (tile * kTile + S::kFetchRows * w);
+        const uint32_t to = tiles + (tile - t0) % kBuf * kTileBytes + w * S::kFetchRows * kQ4Row;
+        if (__builtin_expect(valid >= S::kFetchRows, 1)) q4_fetch_rows<kCausal>(from, lane16, to);
+        else q4_fetch_some(from, valid, l, to);
     };
+    if (S::kWaves == 4 || w < 4) find_rows();
 #pragma unroll 1
-    for (int d = 0; d < kBuf - 1; ++d) issue(t0 + d, d);
+    for (int d = 0; d < kBuf - 2; ++d) issue(t0 + d);
 
     Query q;
-    float m = -INFINITY, mu = 0.f, lsum = 0.f;
+    float m = kNone, mu = 0.f, lsum = 0.f;
     const int qrow = min(16 * rw + c16, sink.rows - 1);
-    load_query(q, A.q + (sink.row0 + qrow) * kMlaRow, t);
-    const int limit = kCausal ? src.len - (A.tokens - 1 - (sink.first_row + qrow) / A.heads) : src.len;
-    f32x16 acc[kRW][kBlocks];
+    {
+        static_assert(2 * kTileBytes + sizeof(lds.val) + sizeof(lds.p) >= 32 * kRW * 1024, "room for the queries");
+        const uint32_t at = tiles + (kBuf - 2) * kTileBytes;
+        stage_query<kRW>(A, sink, at, lds.qscale);
 #pragma unroll
-    for (int rb = 0; rb < kRW; ++rb)
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[rb][b][i] = 0.f;
+        for (int n = 0; n < 2; ++n)
+            q.pe[n] = __builtin_bit_cast(
+                bf16x8, *reinterpret_cast<const u32x4*>(A.q + (sink.row0 + qrow) * kMlaRow + kMlaLatent + 32 * n + 8 * t));
+        raw_barrier();
+        take_query<kRW>(q, at, lds.qscale, 16 * rw + c16, t);
+        raw_barrier();
+        issue(t0 + kBuf - 2);
+    }
+    // (rows from `end` on, which belong to others or to nobody, are behind every limit)
+    const int limit = min(end, kCausal ? src.len - (A.tokens - 1 - (sink.first_row + qrow) / A.heads) : src.len);
+    const int all_see = min(end, kCausal ? src.len - (A.tokens - 1) : src.len);
+    // block kBlocks rb + b: 32 query rows by 32 channels
+    static_assert(kRW * kBlocks == 4, "the accumulation registers");
+    each<64>([](auto x) { q4_acc_clear<decltype(x)::value>(); });
 
     // this lane's addresses, from a tile's start
-    const uint32_t krow = (kw * kTB * 16 + c16) * kQ4Row;                // the row it scores
-    const uint32_t drow = c16 * kQ4Row + kQ4ScaleAt / kWaves * w + 16 * t;   // its part of the row it unpacks
-    const uint32_t dscale = c16 * kQ4Row + kQ4ScaleAt + 4 * w;
-    const uint32_t vput = val + c16 * kValRow;
+    const uint32_t krow = (kw * 16 + c16) * kQ4Row;                          // the row it scores
+    const int urow = l % S::kValRows, ugroup = l / S::kValRows;              // what it unpacks
+    const uint32_t drow = urow * kQ4Row + S::kChannels / 2 * w + 16 * ugroup;
+    const int dbyte = S::kChannels / kQ4Group * w;
+    const uint32_t dscale = urow * kQ4Row + kQ4ScaleAt + (dbyte & ~3);
+    const int dshift = 8 * ((dbyte & 3) + ugroup);
+    const uint32_t vput = val + urow * kValRow + 16 * (4 * ugroup ^ val_swz<kValRow>(urow));
     const int vr = 8 * g + (c16 >> 2), vlow = 2 * (t & 1) + ((c16 >> 1) & 1);
     uint32_t vget[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-        vget[n] = val + (vr + 4 * n) * kValRow + 16 * (vlow ^ val_swz(vr + 4 * n)) + 8 * (c16 & 1);
-    const uint32_t pput = lds_addr(&lds.p[0][rw >> 1][kw * kTB][16 * (rw & 1) + c16 + 32 * (t >> 1)]) + 8 * (t & 1);
-    const bool idle = 16 * rw >= sink.rows;
+        vget[n] = val + (vr + 4 * n) * kValRow + 16 * (vlow ^ val_swz<kValRow>(vr + 4 * n)) + 8 * (c16 & 1);
+    const uint32_t pput = lds_addr(&lds.p[0][rw >> 1][kw][16 * (rw & 1) + c16 + 32 * (t >> 1)]) + 8 * (t & 1);
+    const uint32_t pget = lds_addr(&lds.p[0][0][0][l]);
+
+    // A tile's stages.  Scores of 16 cached rows: operands by halves, products.
+    f32x4 hi, lo;   // two chains: a product waits for the one before
+    uint32_t kscale;
+    u32x4 k4[4];
+    bf16x8 pe[2];
+    auto read_scale = [&](uint32_t tile) { kscale = lds_read4(tile + krow + kQ4ScaleAt + 4 * t); };
+    auto read_rows = [&](uint32_t tile, int half) {
+#pragma unroll
+        for (int n = 2 * half; n < 2 * half + 2; ++n) k4[n] = lds_read_u4(tile + krow + 64 * t + 16 * n);
+    };
+    auto read_pe = [&](uint32_t tile) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) pe[n] = lds_read16(tile + krow + kQ4PeAt + 64 * n + 16 * t);
+    };
+    auto score = [&](auto nn) {
+        constexpr int n = decltype(nn)::value;
+        q4_score<n, 0>(hi, k4[n], q.hi[n], kscale, q.scale);
+        q4_score<n, 1>(lo, k4[n], q.lo[n], kscale, q.scale);
+    };
+    auto score_pe = [&]() {
+        q4_score_pe(hi, pe[0], q.pe[0]);
+        q4_score_pe(lo, pe[1], q.pe[1]);
+    };
+    auto scores = [&]() { each<4>(score); };
+    // Values: a lane unpacks a group of 32 channels of a row.
+    constexpr int kParts = kTile / S::kValRows;
+    u32x4 codes[kParts];
+    uint32_t scales[kParts];
+    auto read_codes = [&](uint32_t tile) {
+#pragma unroll
+        for (int x = 0; x < kParts; ++x) {
+            codes[x] = lds_read_u4(tile + drow + x * S::kValRows * kQ4Row);
+            scales[x] = lds_read4(tile + dscale + x * S::kValRows * kQ4Row);
+        }
+    };
+    float unit;
+    auto unpack_scale = [&](int x) {
+        // NaN groups are left out here: they have made the scores of all who see
+        // them NaN, and no others may meet them as 0 x NaN
+        const uint32_t sb = (scales[x] >> dshift) & 255;
+        unit = q4_scale(sb == kQ4Bad ? 0 : sb);
+    };
+    auto unpack = [&](int x, int j) { lds_write_u4(vput ^ (16 * j), q4_eight(codes[x][j], unit)); };
+    auto unpack_all = [&](int x) {
+        unpack_scale(x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack(x, j);
+    };
+    // The products of 16 cached rows with their probabilities.
+    bf16x8 v[kBlocks], pr[kRW];
+    auto read_p = [&](int i, int step) {
+#pragma unroll
+        for (int rb = 0; rb < kRW; ++rb)
+            pr[rb] = lds_read16(pget + (i & 1) * sizeof(lds.p[0]) + rb * sizeof(lds.p[0][0]) +
+                                step * sizeof(lds.p[0][0][0]));
+    };
+    auto read_values = [&](int step) {
+        const uint32_t at = kParts == 1 ? step * 16 * kValRow : 0;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const u32x2 y = lds_read_tr8((vget[0] ^ (64 * b)) + at), z = lds_read_tr8((vget[1] ^ (64 * b)) + at);
+            v[b] = __builtin_bit_cast(bf16x8, u32x4{y[0], y[1], z[0], z[1]});
+        }
+    };
+    auto add_values = [&](auto nn) {   // the n-th of four
+        constexpr int n = decltype(nn)::value, b = n / kRW, rb = n % kRW;
+        q4_acc_product<kBlocks * rb + b>(v[b], pr[rb]);
+    };
+    // Softmax of tile i's scores against the reference that stands.
+    f32x4 s;
+    float top, before;
+    auto store_p = [&](int i) {
+        f32x4 e;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            e[x] = __builtin_amdgcn_exp2f(fmaf(s[x], c, -mu));
+            lsum += e[x];
+        }
+        lds_write_u2(pput + (i & 1) * sizeof(lds.p[0]), u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])});
+    };
+    auto mask = [&](int i) {
+        const int k0 = (t0 + i) * kTile;
+        q4_score_done(hi, lo);
+        s = hi + lo;
+        if (__builtin_expect(k0 + kTile > all_see, 0)) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (k0 + 16 * kw + 4 * t + x >= limit) s[x] = -INFINITY;
+        }
+    };
+    // The reference moves only when a row outgrows it by 2^8: the probabilities go
+    // out against the one that stands, and again where it moves.
+    auto probabilities = [&](int i) {
+        before = lsum;
+        store_p(i);
+    };
+    auto look = [&](int i) {
+        top = max_over_quarters(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+        if (__any((top - m) * c > 8.f)) lds.moved[i & 1] = turn + i;
+    };
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
     wait_vm<(kBuf - 2) * kQ4Fetch>();
     raw_barrier();
-    f32x4 s[kTB];
-    // this wave's scores of the tile at `tile`
-    auto scores = [&](uint32_t tile) {
-#pragma unroll
-        for (int tb = 0; tb < kTB; ++tb) {
-            const uint32_t row = tile + krow + tb * 16 * kQ4Row;
-            const int sc = int(lds_read4(row + kQ4ScaleAt + 4 * t));
-            f32x4 hi = zero4(), lo = zero4();   // (two chains: each product waits for the one before)
-            each<4>([&](auto mm) {
-                constexpr int n = decltype(mm)::value;
-                const u32x4 k4 = lds_read_u4(row + 64 * t + 16 * n);
-                const i32x8 a = {int(k4[0]), int(k4[1]), int(k4[2]), int(k4[3]), 0, 0, 0, 0};
-                hi = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.hi[n], hi, 4, 0, n, sc, 0, int(q.scale));
-                lo = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, q.lo[n], lo, 4, 0, n, sc, 1, int(q.scale));
-            });
-            hi = mfma_bf16(lds_read16(row + kQ4PeAt + 16 * t), q.pe[0], hi);
-            lo = mfma_bf16(lds_read16(row + kQ4PeAt + 64 + 16 * t), q.pe[1], lo);
-            s[tb] = hi + lo;
-        }
-    };
-    if (!idle) scores(tiles);
+    read_scale(tiles);
+    read_rows(tiles, 0);
+    read_rows(tiles, 1);
+    read_pe(tiles);
+    scores();
+    score_pe();
+    read_codes(tiles);
+    mask(0);
+    probabilities(0);
+    look(0);
+    unpack_all(0);
     const int n_tiles = t1 - t0;
+#pragma unroll 1
     for (int i = 0; i < n_tiles; ++i) {
-        const int k0 = (t0 + i) * kTile, buf = i % kBuf, flag = i % 3;
-        const uint32_t tile = tiles + buf * kTileBytes;
-        const uint32_t pbuf = (i & 1) * sizeof(lds.p[0]);
-        // 16 rows of this wave's 128 channels: a lane unpacks a group of a row
-        u32x4 codes[kTile / kValRows];
-        float unit[kTile / kValRows];
-#pragma unroll
-        for (int ch = 0; ch < kTile / kValRows; ++ch) {
-            const uint32_t at = tile + ch * kValRows * kQ4Row;
-            const uint32_t sb = (lds_read4(at + dscale) >> (8 * t)) & 255;
-            codes[ch] = lds_read_u4(at + drow);
-            // NaN groups are left out here: they have made the scores of all who
-            // see them NaN, and no others may meet them as 0 x NaN
-            unit[ch] = q4_scale(sb == kQ4Bad ? 0 : sb);
-        }
-        auto unpack = [&](int ch) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                lds_write_u4(vput + 16 * ((4 * t + j) ^ val_swz(c16)), q4_eight(codes[ch][j], unit[ch]));
-        };
-        auto store_p = [&]() {
-#pragma unroll
-            for (int tb = 0; tb < kTB; ++tb) {
-                f32x4 e;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    e[x] = __builtin_amdgcn_exp2f(fmaf(s[tb][x], c, -mu));
-                    lsum += e[x];
-                }
-                lds_write_u2(pput + pbuf + tb * sizeof(lds.p[0][0][0]),
-                             u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])});
-            }
-        };
-        float top = -INFINITY, before = 0.f;
-        if (!idle) {
-            if (k0 + kTile > all_see) {
-#pragma unroll
-                for (int tb = 0; tb < kTB; ++tb)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (k0 + 16 * (kw * kTB + tb) + 4 * t + x >= limit) s[tb][x] = -INFINITY;
-            }
-#pragma unroll
-            for (int tb = 0; tb < kTB; ++tb)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) top = fmaxf(top, s[tb][x]);
-            top = max_over_quarters(top);
-            before = lsum;
-            // the reference moves only when a row outgrows it by 2^8: the
-            // probabilities go out against the one that stands, and again where it moves
-            store_p();
-            if (__any((top - m) * c > 8.f || (m == -INFINITY && top > m)) && l == 0) lds.moved[flag] = 1;
-        }
-        if (threadIdx.x == 0) lds.moved[flag == 2 ? 0 : flag + 1] = 0;
-        unpack(0);
         wait_vm<(kBuf - 3) * kQ4Fetch>();   // this wave's part of the next tile
-        raw_barrier();
-        const int moved = lds.moved[flag];
-        // the tile before is read: its memory takes the next one
-        issue(t0 + i + kBuf - 1, (i + kBuf - 1) % kBuf);
-        if (__builtin_amdgcn_readfirstlane(moved)) {
-            if constexpr (kKW > 1) {
-                if (t == 0) lds.top[w][c16] = top;
-                raw_barrier();
-            }
-            if (!idle) {
-                float mn = fmaxf(m, top);
-                if constexpr (kKW > 1) {
-#pragma unroll
-                    for (int k = 0; k < kKW; ++k) mn = fmaxf(mn, lds.top[k * kRowWaves + rw][c16]);
-                }
-                const float mun = mn == -INFINITY ? 0.f : mn * c;
-                const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
-                m = mn;
-                mu = mun;
-                lsum = before * a;
-                if (kw == 0 && t == 0) lds.factor[16 * rw + c16] = a;
-                store_p();
-            }
+        raw_barrier();                      // everyone's; the tile before is read
+        const uint32_t next = tiles + ((i + 1) % kBuf) * kTileBytes;
+        const int moved = lds.moved[i & 1];
+        // The scores of the next tile (none behind the last) beside this one's sums,
+        // in this order: LDS reads well before their use, few operands at a time.
+        read_values(0);
+        read_scale(next);
+        read_rows(next, 0);
+        fence();
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(moved) == turn + i, 0)) {
+            if (t == 0) lds.top[w][c16] = top;
             raw_barrier();
+            float mn = fmaxf(m, top);
 #pragma unroll
-            for (int rb = 0; rb < kRW; ++rb) {
-                const float f = lds.factor[32 * rb + c32];
+            for (int k = 0; k < S::kKeyWaves; ++k) mn = fmaxf(mn, lds.top[k * S::kRowWaves + rw][c16]);
+            const float mun = mn == kNone ? 0.f : mn * c;
+            const float a = m == kNone ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
+            m = mn;
+            mu = mun;
+            lsum = before * a;
+            if (kw == 0 && t == 0) lds.factor[16 * rw + c16] = a;
+            store_p(i);
+            raw_barrier();
+            float f[kRW];
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) acc[rb][b][x] *= f;
-            }
+            for (int rb = 0; rb < kRW; ++rb) f[rb] = lds.factor[32 * rb + c32];
+            q4_acc_settle();
+            each<64>([&](auto x) { q4_acc_scale<decltype(x)::value>(f[decltype(x)::value / (16 * kBlocks)]); });
         }
-        // the scores of the next tile (zeros behind the last) beside this one's sums
-        const uint32_t next = tiles + (buf + 1 == kBuf ? 0 : buf + 1) * kTileBytes;
-        if (!idle) scores(next);
+        read_p(i, 0);
+        fence();
+        // (matrix instructions run beside the ordinary ones that follow them)
+        if constexpr (kParts > 1) unpack_scale(1);
+        each<4>([&](auto nn) {
+            add_values(nn);
+            if constexpr (kParts > 1) unpack(1, decltype(nn)::value);
+            fence();
+        });
+        read_rows(next, 1);
+        read_p(i, 1);
+        read_values(1);
+        read_pe(next);
+        fence();
+        scores();
+        score_pe();
+        issue(t0 + i + kBuf - 1);
+        read_codes(next);
+        fence();
+        add_values(std::integral_constant<int, 0>{});
+        fence();
+        mask(i + 1);
+        fence();
+        add_values(std::integral_constant<int, 1>{});
+        fence();
+        probabilities(i + 1);
+        fence();
+        add_values(std::integral_constant<int, 2>{});
+        fence();
+        look(i + 1);
+        unpack_scale(0);
+        fence();
+        add_values(std::integral_constant<int, 3>{});
 #pragma unroll
-        for (int ch = 0; ch < kTile / kValRows; ++ch) {
-            if (ch > 0) unpack(ch);
-            bf16x8 pr[kRW];
-#pragma unroll
-            for (int rb = 0; rb < kRW; ++rb) pr[rb] = __builtin_bit_cast(bf16x8, lds.p[i & 1][rb][ch][l]);
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const u32x2 x = lds_read_tr8(vget[0] ^ (64 * b));
-                const u32x2 y = lds_read_tr8(vget[1] ^ (64 * b));
-                const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
-#pragma unroll
-                for (int rb = 0; rb < kRW; ++rb)
-                    acc[rb][b] = mfma32(v, pr[rb], acc[rb][b]);
-            }
-        }
+        for (int j = 0; j < 4; ++j) unpack(0, j);
     }
     wait_vm<0>();   // the tiles behind the last: nothing may land later
-    lsum = sum_over_quarters(lsum);
-    if (t == 0) {
-        lds.l[w][c16] = lsum;
-        if (kw == 0) lds.mu[16 * rw + c16] = m == -INFINITY ? -INFINITY : mu;
-    }
     raw_barrier();
-#pragma unroll
-    for (int rb = 0; rb < kRW; ++rb) {
-        float total = 0.f;
-#pragma unroll
-        for (int k = 0; k < kKW; ++k) total += lds.l[k * kRowWaves + 2 * rb + (c32 >> 4)][c16];
-        const int lr = 32 * rb + c32;
-        if (w == rb && g == 0 && lr < sink.rows) {
-            const float x = lds.mu[lr];
-            if (!sink.final) *reinterpret_cast<f32x2*>(sink.ml + 2 * lr) = f32x2{x, total};
-            else if (A.lse) A.lse[sink.row0 + lr] = total == 0.f ? -INFINITY : fmaf(x, kLn2, logf(total));
+    {
+        // (addresses computed here: kept from the start they would crowd out the loop)
+        const int l = here(threadIdx.x & 63), c16 = l & 15, t = l >> 4, c32 = l & 31, g = l >> 5;
+        lsum = sum_over_quarters(lsum);
+        if (t == 0) {
+            lds.l[w][c16] = lsum;
+            if (kw == 0) lds.mu[16 * rw + c16] = m == kNone ? -INFINITY : mu;
         }
-        const float inv = !sink.final ? 1.f : total == 0.f ? 0.f : 1.f / total;
-        // 32 channels at a time by way of LDS, so that they leave row by row
+        raw_barrier();
+        q4_acc_settle();
+        each<kRW>([&](auto rr) {
+            constexpr int rb = decltype(rr)::value;
+            float total = 0.f;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const f32x16& a = acc[rb][b];
-                const f32x4 y = {a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv, a[4 * x + 3] * inv};
-                lds_write_u4(val + c32 * 128 + 16 * ((2 * x + g) ^ (c32 & 7)), __builtin_bit_cast(u32x4, y));
+            for (int k = 0; k < S::kKeyWaves; ++k) total += lds.l[k * S::kRowWaves + 2 * rb + (c32 >> 4)][c16];
+            const int lr = 32 * rb + c32;
+            if (w == rb && g == 0 && lr < sink.rows) {
+                const float x = lds.mu[lr];
+                if (!sink.final) *reinterpret_cast<f32x2*>(sink.ml + 2 * lr) = f32x2{x, total};
+                else if (A.lse) A.lse[sink.row0 + lr] = total == 0.f ? -INFINITY : fmaf(x, kLn2, logf(total));
             }
+            const float inv = !sink.final ? 1.f : total == 0.f ? 0.f : 1.f / total;
+            // 32 channels at a time by way of LDS, so that they leave row by row
+            each<kBlocks>([&](auto bb) {
+                constexpr int b = decltype(bb)::value;
+                each<4>([&](auto xx) {
+                    constexpr int x = decltype(xx)::value, r = 16 * (kBlocks * rb + b) + 4 * x;
+                    const f32x4 y = {q4_acc_get<r>() * inv, q4_acc_get<r + 1>() * inv, q4_acc_get<r + 2>() * inv,
+                                     q4_acc_get<r + 3>() * inv};
+                    lds_write_u4(val + c32 * 128 + 16 * ((2 * x + g) ^ (c32 & 7)), __builtin_bit_cast(u32x4, y));
+                });
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = 8 * x + (l >> 3), row = 32 * rb + r;
-                const f32x4 y = __builtin_bit_cast(
-                    f32x4, lds_read_u4(val + r * 128 + 16 * ((l & 7) ^ (r & 7))));
-                if (row >= sink.rows) continue;
-                const int ch = kValChannels * w + 32 * b + 4 * (l & 7);
-                if (sink.final)
-                    *reinterpret_cast<u32x2*>(A.o + (sink.row0 + row) * kMlaLatent + ch) =
-                        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-                else
-                    *reinterpret_cast<f32x4*>(sink.part + size_t(row) * kMlaLatent + ch) = y;
-            }
-        }
+                for (int x = 0; x < 4; ++x) {
+                    const int r = 8 * x + (l >> 3), row = 32 * rb + r;
+                    const f32x4 y = __builtin_bit_cast(
+                        f32x4, lds_read_u4(val + r * 128 + 16 * ((l & 7) ^ (r & 7))));
+                    if (row >= sink.rows) continue;
+                    const int ch = S::kChannels * w + 32 * b + 4 * (l & 7);
+                    if (sink.final)
+                        *reinterpret_cast<u32x2*>(A.o + (sink.row0 + row) * kMlaLatent + ch) =
+                            u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                    else
+                        *reinterpret_cast<f32x4*>(sink.part + size_t(row) * kMlaLatent + ch) = y;
+                }
+            });
+        });
     }
+    turn += n_tiles + 1;
     raw_barrier();   // the next piece writes what this one has read
 }
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 template <int kRW>
-__global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
+    constexpr int kThreads = Shape<kRW>::kThreads, kWaves = Shape<kRW>::kWaves;
     const int l = threadIdx.x & 63, w = wave_id(), wg = blockIdx.x;
+    const int workgroups = gridDim.x;
 
     auto block_sum = [&](int x, int& before) {   // x over the workgroup
         int s = x;
@@ -434,7 +538,7 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
         return __builtin_amdgcn_readfirstlane(total);
     };
     auto tiles_at = [&](int b) { return b < A.batch ? tiles_of(clamp_len(A, b)) : 0; };
-    if (threadIdx.x < 3) lds.moved[threadIdx.x] = 0;
+    if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
     int n0 = tiles_at(threadIdx.x);
     int before0;
     int total0 = block_sum(n0, before0);
@@ -445,11 +549,11 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
     }
     total *= A.row_blocks;
     if (total == 0) return;
-    const int share = (total + kQ4Workgroups - 1) / kQ4Workgroups;
+    const int share = (total + workgroups - 1) / workgroups;
     const int units = A.batch * A.row_blocks;
     int per = max(share, min(A.min_tiles, (total + units - 1) / units));
     bool apart = false;
-    if (units <= kQ4Workgroups && A.batch <= kThreads && share < 1 << 20) {
+    if (units <= workgroups && A.batch <= kThreads && share < 1 << 20) {
         int most = n0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
@@ -458,13 +562,13 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
         most = __builtin_amdgcn_readfirstlane(most);
-        int each = max(A.min_tiles, total / (kQ4Workgroups - units / 2) + 1);
+        int each = max(A.min_tiles, total / (workgroups - units / 2) + 1);
         for (int tries = 0; tries < 2 && !apart && each <= max(share, A.min_tiles) + kPieceTiles; ++tries) {
             if (most <= each + 2) each = most;
             const int padded = (n0 + each - 1) / each * each;
             int before;
             const int sum = block_sum(padded, before);
-            if (sum * A.row_blocks <= each * kQ4Workgroups) {
+            if (sum * A.row_blocks <= each * workgroups) {
                 apart = true;
                 per = each;
                 n0 = padded;
@@ -496,7 +600,7 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
     int first = __builtin_amdgcn_readfirstlane(lds.first);
 
     const int unit_rows = A.tokens * A.heads;
-    int at = begin;
+    int at = begin, turn = 1;   // (turn: a number for each tile, for lds.moved)
     while (at < end) {
         const int b = unit / A.row_blocks, blk = unit - b * A.row_blocks;
         const int len = __builtin_amdgcn_readfirstlane(clamp_len(A, b));
@@ -519,7 +623,7 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
             A.meta[2 * unit] = sink.final ? -1 : wg;
             A.meta[2 * unit + 1] = (at + n - 1) / per;
         }
-        piece<kRW, true>(A, lds, Source{A.table + int64_t(b) * A.table_width, len}, first, last, sink);
+        piece<kRW, true>(A, lds, Source{A.table + int64_t(b) * A.table_width, len}, first, last, sink, turn);
         if (apart) break;
         at += last - first;
         first = 0;
@@ -529,7 +633,7 @@ __global__ __launch_bounds__(kThreads, 2) void mla_decode_q4_kernel(const MlaDec
 
 // The prefix: every block of 32 kRW query rows walks all prefix rows.
 template <int kRW>
-__global__ __launch_bounds__(kThreads, 2) void mla_prefix_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_prefix_q4_kernel(const MlaDecodeArgs A) {
     __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
     const int wg = blockIdx.x;
     const int rows = A.batch * A.tokens * A.heads;
@@ -537,7 +641,8 @@ __global__ __launch_bounds__(kThreads, 2) void mla_prefix_q4_kernel(const MlaDec
     const int total = A.prefix_units * n;
     int at = A.prefix_per * wg;
     const int end = min(at + A.prefix_per, total);
-    if (threadIdx.x < 3) lds.moved[threadIdx.x] = 0;
+    int turn = 1;
+    if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
     __syncthreads();
     while (at < end) {
         const int unit = at / n, first = at - unit * n;
@@ -550,16 +655,16 @@ __global__ __launch_bounds__(kThreads, 2) void mla_prefix_q4_kernel(const MlaDec
         sink.rows = min(32 * kRW, rows - unit * 32 * kRW);
         sink.part = A.pre_part + size_t(slot) * kMlaLatent * 32 * kRW;
         sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRW;
-        piece<kRW, false>(A, lds, Source{A.prefix_table, A.prefix_len}, first, last, sink);
+        piece<kRW, false>(A, lds, Source{A.prefix_table, A.prefix_len}, first, last, sink, turn);
         at += last - first;
     }
 }
 
 // Joins the partial sums of a query row, a wave per row (eight channels a lane).
-__global__ __launch_bounds__(kThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
+__global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
     const int l = threadIdx.x & 63;
     const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
-    const int row = blockIdx.x * (kThreads / 64) + wave_id();
+    const int row = blockIdx.x * (kJoinThreads / 64) + wave_id();
     if (row >= A.batch * unit_rows) return;
     const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
     const int stride = 32 * A.row_waves;
@@ -632,14 +737,14 @@ __global__ __launch_bounds__(kThreads) void mla_join_q4_kernel(const MlaDecodeAr
 
 template <int kRW>
 void launch_private(const MlaDecodeArgs& A, hipStream_t stream) {
-    mla_decode_q4_kernel<kRW><<<dim3(kQ4Workgroups), dim3(kThreads), 0, stream>>>(A);
+    mla_decode_q4_kernel<kRW><<<dim3(kQ4Workgroups / kRW), dim3(Shape<kRW>::kThreads), 0, stream>>>(A);
 }
 
 template <int kRW>
 void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
     const int total = A.prefix_units * ((A.prefix_len + kTile - 1) / kTile);
     mla_prefix_q4_kernel<kRW><<<dim3(unsigned((total + A.prefix_per - 1) / A.prefix_per)),
-                                dim3(kThreads), 0, stream>>>(A);
+                                dim3(Shape<kRW>::kThreads), 0, stream>>>(A);
 }
 
 }  // namespace
@@ -654,7 +759,7 @@ hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
     else launch_private<1>(A, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int rows = A.batch * A.tokens * A.heads;
-    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kThreads), 0, stream>>>(A);
+    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
