@@ -390,6 +390,9 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     const int n_tiles = t1 - t0;
 #pragma unroll 1
     for (int i = 0; i < n_tiles; ++i) {
+        // (two workgroups of a CU take turns: left alone the older one goes first)
+        if ((i ^ (blockIdx.x >> 8)) & 1) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
         wait_vm<(kBuf - 3) * kQ4Fetch>();   // this wave's part of the next tile
         raw_barrier();                      // everyone's; the tile before is read
         const uint32_t next = tiles + ((i + 1) % kBuf) * kTileBytes;
@@ -539,22 +542,30 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(
     };
     auto tiles_at = [&](int b) { return b < A.batch ? tiles_of(clamp_len(A, b)) : 0; };
     if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
-    int n0 = tiles_at(threadIdx.x);
-    int before0;
-    int total0 = block_sum(n0, before0);
+    // A unit's second and later pieces cost their workgroup nothing that it does not
+    // pay anyway (queries in, sums out); a workgroup that goes on to another unit pays
+    // again, as much as kPieceTiles tiles.  So the line that is cut into equal
+    // shares holds that many places before each unit's tiles.
+    const int n0 = tiles_at(threadIdx.x);
+    int head = kPieceTiles, before0;
+    auto places = [&](int n) { return n > 0 ? n + head : 0; };
+    int x0 = places(n0);
+    int total0 = block_sum(x0, before0);
     int total = total0;
     for (int b0 = kThreads; b0 < A.batch; b0 += kThreads) {
         int before;
-        total += block_sum(tiles_at(b0 + int(threadIdx.x)), before);
+        total += block_sum(places(tiles_at(b0 + int(threadIdx.x))), before);
     }
     total *= A.row_blocks;
     if (total == 0) return;
-    const int share = (total + workgroups - 1) / workgroups;
     const int units = A.batch * A.row_blocks;
-    int per = max(share, min(A.min_tiles, (total + units - 1) / units));
+    int per = max((total + workgroups - 1) / workgroups, A.min_tiles);
+    // Where the workgroups suffice for it none goes on to another unit: the units'
+    // tiles are counted up to multiples of a share then, one as large as that line's
+    // at most.
     bool apart = false;
-    if (units <= workgroups && A.batch <= kThreads && share < 1 << 20) {
-        int most = n0;
+    if (units <= workgroups && A.batch <= kThreads) {
+        int most = n0, tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
         if (l == 0) lds.scan[kWaves + w] = most;
@@ -562,36 +573,41 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
         most = __builtin_amdgcn_readfirstlane(most);
-        int each = max(A.min_tiles, total / (workgroups - units / 2) + 1);
-        for (int tries = 0; tries < 2 && !apart && each <= max(share, A.min_tiles) + kPieceTiles; ++tries) {
-            if (most <= each + 2) each = most;
-            const int padded = (n0 + each - 1) / each * each;
+        {
+            int before;
+            tiles = block_sum(n0, before);
+        }
+        int share = max(A.min_tiles, tiles * A.row_blocks / (workgroups - units / 2) + 1);
+        for (int tries = 0; tries < 2 && !apart && share <= per; ++tries) {
+            if (most <= share + 2) share = most;
+            const int padded = (n0 + share - 1) / share * share;
             int before;
             const int sum = block_sum(padded, before);
-            if (sum * A.row_blocks <= each * workgroups) {
+            if (sum * A.row_blocks <= share * workgroups) {
                 apart = true;
-                per = each;
-                n0 = padded;
+                per = share;
+                head = 0;
+                x0 = padded;
                 before0 = before;
                 total0 = sum;
                 total = sum * A.row_blocks;
             }
-            each += each / 8 + 1;
+            share += share / 8 + 1;
         }
     }
     if (int64_t(per) * wg >= total) return;
     const int begin = per * wg, end = min(begin + per, total);
     for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
         const int b = b0 + int(threadIdx.x);
-        int n = n0, before = before0, sum = total0;
+        int x = x0, before = before0, sum = total0;
         if (b0 > 0) {
-            n = tiles_at(b);
-            sum = block_sum(n, before);
+            x = places(tiles_at(b));
+            sum = block_sum(x, before);
         }
         const int at = begin - (seen + before) * A.row_blocks;
-        if (n > 0 && at >= 0 && at < n * A.row_blocks) {
-            lds.unit = b * A.row_blocks + at / n;
-            lds.first = at % n;
+        if (x > 0 && at >= 0 && at < x * A.row_blocks) {
+            lds.unit = b * A.row_blocks + at / x;
+            lds.first = at % x;
         }
         seen += sum;
     }
@@ -609,21 +625,25 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(
             ++unit;
             continue;
         }
-        const int last = min(first + (end - at), n);
-        const bool whole = first == 0 && last == n;
-        const int slot = first == 0 ? unit : units + wg;
-        Sink sink;
-        sink.final = whole && !A.prefix_len;
-        sink.first_row = 32 * kRW * blk;
-        sink.row0 = int64_t(b) * unit_rows + sink.first_row;
-        sink.rows = min(32 * kRW, unit_rows - sink.first_row);
-        sink.part = A.part + size_t(slot) * kMlaLatent * 32 * kRW;
-        sink.ml = A.part_ml + size_t(slot) * 2 * 32 * kRW;
-        if (first == 0 && threadIdx.x == 0) {
-            A.meta[2 * unit] = sink.final ? -1 : wg;
-            A.meta[2 * unit + 1] = (at + n - 1) / per;
+        const int last = min(first + (end - at), n + head);
+        const int t0 = max(first - head, 0), t1 = last - head;
+        if (t0 < t1) {
+            const bool whole = t0 == 0 && t1 == n;
+            const int slot = t0 == 0 ? unit : units + wg;
+            Sink sink;
+            sink.final = whole && !A.prefix_len;
+            sink.first_row = 32 * kRW * blk;
+            sink.row0 = int64_t(b) * unit_rows + sink.first_row;
+            sink.rows = min(32 * kRW, unit_rows - sink.first_row);
+            sink.part = A.part + size_t(slot) * kMlaLatent * 32 * kRW;
+            sink.ml = A.part_ml + size_t(slot) * 2 * 32 * kRW;
+            if (t0 == 0 && threadIdx.x == 0) {
+                // the workgroups that hold this unit's later pieces
+                A.meta[2 * unit] = sink.final ? -1 : wg;
+                A.meta[2 * unit + 1] = (at - first + n + head - 1) / per;
+            }
+            piece<kRW, true>(A, lds, Source{A.table + int64_t(b) * A.table_width, len}, t0, t1, sink, turn);
         }
-        piece<kRW, true>(A, lds, Source{A.table + int64_t(b) * A.table_width, len}, first, last, sink, turn);
         if (apart) break;
         at += last - first;
         first = 0;
