@@ -12,7 +12,7 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 4, kJoinRows = 128;
 constexpr int kPieceTiles = 6;
 
 // A workgroup of 32 kRW query rows: 4 kRW waves.
@@ -514,12 +514,11 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
+// Workgroup `wg` of those that share out the sequences' tiles.
 template <int kRW>
-__global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(const MlaDecodeArgs A) {
-    __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
+__device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>& lds, int wg, int workgroups) {
     constexpr int kThreads = Shape<kRW>::kThreads, kWaves = Shape<kRW>::kWaves;
-    const int l = threadIdx.x & 63, w = wave_id(), wg = blockIdx.x;
-    const int workgroups = gridDim.x;
+    const int l = threadIdx.x & 63, w = wave_id();
 
     auto block_sum = [&](int x, int& before) {   // x over the workgroup
         int s = x;
@@ -541,7 +540,6 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(
         return __builtin_amdgcn_readfirstlane(total);
     };
     auto tiles_at = [&](int b) { return b < A.batch ? tiles_of(clamp_len(A, b)) : 0; };
-    if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
     // A unit's second and later pieces cost their workgroup nothing that it does not
     // pay anyway (queries in, sums out); a workgroup that goes on to another unit pays
     // again, as much as kPieceTiles tiles.  So the line that is cut into equal
@@ -653,17 +651,13 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(
 
 // The prefix: every block of 32 kRW query rows walks all prefix rows.
 template <int kRW>
-__global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_prefix_q4_kernel(const MlaDecodeArgs A) {
-    __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
-    const int wg = blockIdx.x;
+__device__ __forceinline__ void walk_prefix(const MlaDecodeArgs& A, Lds<kRW>& lds, int wg) {
     const int rows = A.batch * A.tokens * A.heads;
     const int n = tiles_of(A.prefix_len);
     const int total = A.prefix_units * n;
     int at = A.prefix_per * wg;
     const int end = min(at + A.prefix_per, total);
     int turn = 1;
-    if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
-    __syncthreads();
     while (at < end) {
         const int unit = at / n, first = at - unit * n;
         const int last = min(first + (end - at), n);
@@ -680,106 +674,175 @@ __global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_prefix_q4_kernel(
     }
 }
 
-// Joins the partial sums of a query row, a wave per row (eight channels a lane).
+// Workgroups before `prefix` walk the prefix, the others the sequences.
+template <int kRW>
+__global__ __launch_bounds__(Shape<kRW>::kThreads, 2) void mla_decode_q4_kernel(const MlaDecodeArgs A, int prefix) {
+    __shared__ __attribute__((aligned(256))) Lds<kRW> lds;
+    if (threadIdx.x < 2) lds.moved[threadIdx.x] = 0;
+    __syncthreads();
+    const int wg = blockIdx.x;
+    if (wg < prefix) walk_prefix<kRW>(A, lds, wg);
+    else walk_sequences<kRW>(A, lds, wg - prefix, int(gridDim.x) - prefix);
+}
+
+// Where the partial sums of a query row lie: `own` pieces of its sequence, then
+// those of the prefix.  (false: it is already written)
+struct Pieces {
+    int own, n;
+    int unit, lr, g0, stride;       // the sequence's: unit, row in it, first workgroup, rows a unit
+    int pu, pr, pg0, pstride;       // the prefix's
+    __device__ __forceinline__ bool find(const MlaDecodeArgs& A, int row) {
+        const int unit_rows = A.tokens * A.heads;
+        const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
+        stride = 32 * A.row_waves;
+        const int blk = urow / stride;
+        lr = urow - blk * stride;
+        unit = b * A.row_blocks + blk;
+        const int len = __builtin_amdgcn_readfirstlane(clamp_len(A, b));
+        own = 0;
+        g0 = 0;
+        if (len > 0) {
+            g0 = __builtin_amdgcn_readfirstlane(A.meta[2 * unit]);
+            if (g0 < 0) return false;
+            own = __builtin_amdgcn_readfirstlane(A.meta[2 * unit + 1]) - g0 + 1;
+        }
+        n = own;
+        pu = pr = pg0 = 0;
+        pstride = 32 * A.prefix_waves;
+        if (A.prefix_len) {
+            const int tiles = tiles_of(A.prefix_len);
+            pu = row / pstride;
+            pr = row - pu * pstride;
+            pg0 = pu * tiles / A.prefix_per;
+            n += (pu * tiles + tiles - 1) / A.prefix_per - pg0 + 1;
+        }
+        return true;
+    }
+    // piece i's statistics and the sums of `row`
+    __device__ __forceinline__ void at(const MlaDecodeArgs& A, int i, const float*& part, const float*& ml) const {
+        const bool mine = i < own;
+        const int slot = mine ? (i == 0 ? unit : A.batch * A.row_blocks + g0 + i)
+                              : (i == own ? pu : A.prefix_units + pg0 + (i - own));
+        const size_t x = size_t(slot) * (mine ? stride : pstride) + (mine ? lr : pr);
+        ml = (mine ? A.part_ml : A.pre_ml) + 2 * x;
+        part = (mine ? A.part : A.pre_part) + x * kMlaLatent;
+    }
+};
+
+// The sums of some of a row's pieces, relative to the largest reference among them.
+template <int kLane>   // channels a lane
+struct Joined {
+    typedef float vec __attribute__((ext_vector_type(kLane)));
+    float top = -INFINITY, total = 0.f;
+    vec sum = 0.f;
+    // pieces first, first + step, .. below n; eight at a time, all loads before their use
+    __device__ __forceinline__ void add(const MlaDecodeArgs& A, const Pieces& P, int first, int step, int ch) {
+        constexpr int kN = 8;
+        for (int i0 = first; i0 < P.n; i0 += kN * step) {
+            f32x2 ml[kN];
+            vec x[kN];
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                const float *part, *m;
+                P.at(A, min(i0 + e * step, P.n - 1), part, m);
+                ml[e] = *reinterpret_cast<const f32x2*>(m);
+                x[e] = *reinterpret_cast<const vec*>(part + ch);
+            }
+            float most = top;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) most = fmaxf(most, ml[e][0]);
+            const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - most);
+            top = most;
+            total *= f;
+            sum *= f;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                if (i0 + e * step >= P.n) break;
+                take(ml[e][0], ml[e][1], x[e]);
+            }
+        }
+    }
+    // (a piece whose scores are all NaN has the reference -inf like one without
+    // keys, but NaN for its sums)
+    __device__ __forceinline__ void take(float m, float l, vec x) {
+        const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+        total = fmaf(l, w, total);
+        sum += x * w;
+    }
+    __device__ __forceinline__ void put(const MlaDecodeArgs& A, int row, int ch, bool first) const {
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        uint32_t out[kLane / 2];
+#pragma unroll
+        for (int k = 0; k < kLane / 2; ++k) out[k] = pack_bf16(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+        __builtin_memcpy(__builtin_assume_aligned(A.o + int64_t(row) * kMlaLatent + ch, 2 * kLane), out, sizeof(out));
+        if (A.lse && first) A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
+    }
+};
+
+// Joins the partial sums of a query row, a wave per row.
 __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
     const int l = threadIdx.x & 63;
-    const int unit_rows = A.tokens * A.heads, units = A.batch * A.row_blocks;
     const int row = blockIdx.x * (kJoinThreads / 64) + wave_id();
-    if (row >= A.batch * unit_rows) return;
-    const int b = row / unit_rows, urow = row - b * unit_rows;   // row in the sequence
-    const int stride = 32 * A.row_waves;
-    const int blk = urow / stride, lr = urow - blk * stride;     // row in the unit
-    const int unit = b * A.row_blocks + blk;
-    const int len = __builtin_amdgcn_readfirstlane(clamp_len(A, b));
-    int np = 0, g0 = 0;                                  // private pieces, first workgroup
-    if (len > 0) {
-        g0 = __builtin_amdgcn_readfirstlane(A.meta[2 * unit]);
-        if (g0 < 0) return;   // already written
-        np = __builtin_amdgcn_readfirstlane(A.meta[2 * unit + 1]) - g0 + 1;
-    }
-    // prefix pieces of this row
-    int pn = 0, pu = 0, pr = 0, pg0 = 0;
-    const int pstride = 32 * A.prefix_waves;
-    if (A.prefix_len) {
-        const int n = tiles_of(A.prefix_len);
-        pu = row / pstride;
-        pr = row - pu * pstride;
-        pg0 = pu * n / A.prefix_per;
-        pn = (pu * n + n - 1) / A.prefix_per - pg0 + 1;
-    }
-    // eight pieces' sums at a time, all loads before their use
-    constexpr int kN = 8;
-    const int n = np + pn;
-    float top = -INFINITY, total = 0.f;
-    f32x4 sum[2] = {zero4(), zero4()};
-    for (int i0 = 0; i0 < n; i0 += kN) {
-        f32x2 ml[kN];
-        f32x4 x[kN][2];
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const int i = min(i0 + e, n - 1);
-            const bool own = i < np;
-            const int slot = own ? (i == 0 ? unit : units + g0 + i)
-                                 : (i == np ? pu : A.prefix_units + pg0 + (i - np));
-            const size_t at = size_t(slot) * (own ? stride : pstride) + (own ? lr : pr);
-            ml[e] = *reinterpret_cast<const f32x2*>((own ? A.part_ml : A.pre_ml) + 2 * at);
-            const float* part = (own ? A.part : A.pre_part) + at * kMlaLatent + 8 * l;
-            x[e][0] = *reinterpret_cast<const f32x4*>(part);
-            x[e][1] = *reinterpret_cast<const f32x4*>(part + 4);
-        }
-        float most = top;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) most = fmaxf(most, ml[e][0]);
-        const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - most);
-        top = most;
-        total *= f;
-        sum[0] *= f;
-        sum[1] *= f;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            if (i0 + e >= n) break;
-            // (a piece whose scores are all NaN has the maximum -inf like one
-            // without keys, but NaN for its sums)
-            const float w = ml[e][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[e][0] - most);
-            total = fmaf(ml[e][1], w, total);
-            sum[0] += x[e][0] * w;
-            sum[1] += x[e][1] * w;
-        }
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    u32x4 out;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        out[k] = pack_bf16(sum[k >> 1][2 * (k & 1)] * inv, sum[k >> 1][2 * (k & 1) + 1] * inv);
-    *reinterpret_cast<u32x4*>(A.o + int64_t(row) * kMlaLatent + 8 * l) = out;
-    if (A.lse && l == 0) A.lse[row] = total == 0.f ? -INFINITY : fmaf(top, kLn2, logf(total));
+    Pieces P;
+    if (row >= A.batch * A.tokens * A.heads || !P.find(A, row)) return;
+    Joined<8> J;
+    J.add(A, P, 0, 1, 8 * l);
+    J.put(A, row, 8 * l, l == 0);
 }
 
-template <int kRW>
-void launch_private(const MlaDecodeArgs& A, hipStream_t stream) {
-    mla_decode_q4_kernel<kRW><<<dim3(kQ4Workgroups / kRW), dim3(Shape<kRW>::kThreads), 0, stream>>>(A);
+// The same for few rows, which may have hundreds of pieces each: a workgroup per
+// row and 128 channels, whose 16 waves share out the pieces.
+__global__ __launch_bounds__(kJoinWide) void mla_join_wide_q4_kernel(const MlaDecodeArgs A) {
+    constexpr int kWaves = kJoinWide / 64;
+    __shared__ float ml[kWaves][2];
+    __shared__ f32x2 sums[kWaves][64];
+    const int l = threadIdx.x & 63, w = wave_id();
+    const int row = blockIdx.x / kJoinSlices, ch = blockIdx.x % kJoinSlices * (kMlaLatent / kJoinSlices) + 2 * l;
+    Pieces P;
+    if (!P.find(A, row)) return;   // (the same for all waves)
+    Joined<2> J;
+    J.add(A, P, w, kWaves, ch);
+    if (l == 0) {
+        ml[w][0] = J.top;
+        ml[w][1] = J.total;
+    }
+    sums[w][l] = J.sum;
+    __syncthreads();
+    if (w > 0) return;
+    const int waves = min(kWaves, P.n);
+    for (int k = 1; k < waves; ++k) J.top = fmaxf(J.top, ml[k][0]);
+    J.total = 0.f;
+    J.sum = 0.f;
+    for (int k = 0; k < waves; ++k) J.take(ml[k][0], ml[k][1], sums[k][l]);
+    J.put(A, row, ch, ch == 0);
 }
 
+// `prefix`: workgroups for the prefix in front; sequences: those of the batch behind.
 template <int kRW>
-void launch_prefix(const MlaDecodeArgs& A, hipStream_t stream) {
-    const int total = A.prefix_units * ((A.prefix_len + kTile - 1) / kTile);
-    mla_prefix_q4_kernel<kRW><<<dim3(unsigned((total + A.prefix_per - 1) / A.prefix_per)),
-                                dim3(Shape<kRW>::kThreads), 0, stream>>>(A);
+hipError_t launch(const MlaDecodeArgs& A, bool prefix, bool sequences, hipStream_t stream) {
+    const int64_t tiles = int64_t(A.prefix_units) * ((A.prefix_len + kTile - 1) / kTile);
+    const int groups = prefix ? int((tiles + A.prefix_per - 1) / A.prefix_per) : 0;
+    mla_decode_q4_kernel<kRW><<<dim3(unsigned(groups + (sequences ? kQ4Workgroups / kRW : 0))),
+                                dim3(Shape<kRW>::kThreads), 0, stream>>>(A, groups);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
-    if (A.prefix_len) {
-        if (A.prefix_waves == 2) launch_prefix<2>(A, stream);
-        else launch_prefix<1>(A, stream);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    if (A.row_waves == 2) launch_private<2>(A, stream);
-    else launch_private<1>(A, stream);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    auto go = [&](int waves, bool prefix, bool sequences) {
+        return waves == 2 ? launch<2>(A, prefix, sequences, stream) : launch<1>(A, prefix, sequences, stream);
+    };
+    const bool together = A.prefix_len > 0 && A.prefix_waves == A.row_waves;
+    if (A.prefix_len > 0 && !together)
+        if (hipError_t e = go(A.prefix_waves, true, false); e != hipSuccess) return e;
+    if (hipError_t e = go(A.row_waves, together, true); e != hipSuccess) return e;
+    // up to two workgroups a CU and slice
     const int rows = A.batch * A.tokens * A.heads;
-    mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
+    if (rows <= kJoinRows)
+        mla_join_wide_q4_kernel<<<dim3(unsigned(rows * kJoinSlices)), dim3(kJoinWide), 0, stream>>>(A);
+    else
+        mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
