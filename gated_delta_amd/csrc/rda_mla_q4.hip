@@ -9,6 +9,8 @@
 // y, e and the rounding are computed in 64 bits.  A step is a quarter or more of
 // a value, so a code must not depend on how a sum was ordered; and the
 // arithmetic hides behind memory.
+#include <type_traits>
+
 #include "rda_mla_q4.h"
 
 namespace rda {
@@ -54,10 +56,35 @@ __device__ __forceinline__ unsigned char* row_at(const MlaRowsQ4Args& A, int t, 
            int64_t(pos & ((1 << A.page_shift) - 1)) * kQ4Row;
 }
 
-__device__ __forceinline__ double shuffle_xor(double x, int d) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __shfl_xor(uint32_t(b), d), hi = __shfl_xor(uint32_t(b >> 32), d);
-    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+// x + the values of the other lanes of the wavefront.
+__device__ __forceinline__ double wave_sum(double x) {
+    auto halves = [](double y) { return __builtin_bit_cast(u32x2, y); };
+    auto dpp = [&](auto ctrl) {
+        constexpr int c = decltype(ctrl)::value;
+        const u32x2 y = halves(x);
+        x += __builtin_bit_cast(double, u32x2{uint32_t(__builtin_amdgcn_update_dpp(0, int(y[0]), c, 0xF, 0xF, false)),
+                                              uint32_t(__builtin_amdgcn_update_dpp(0, int(y[1]), c, 0xF, 0xF, false))});
+    };
+    dpp(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+    dpp(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+    dpp(std::integral_constant<int, 0x141>{});   // row_half_mirror
+    dpp(std::integral_constant<int, 0x140>{});   // row_mirror
+    u32x2 y = halves(x);
+    auto a = __builtin_amdgcn_permlane16_swap(y[0], y[0], false, false);
+    auto b = __builtin_amdgcn_permlane16_swap(y[1], y[1], false, false);
+    x = __builtin_bit_cast(double, u32x2{a[0], b[0]}) + __builtin_bit_cast(double, u32x2{a[1], b[1]});
+    y = halves(x);
+    a = __builtin_amdgcn_permlane32_swap(y[0], y[0], false, false);
+    b = __builtin_amdgcn_permlane32_swap(y[1], y[1], false, false);
+    return __builtin_bit_cast(double, u32x2{a[0], b[0]}) + __builtin_bit_cast(double, u32x2{a[1], b[1]});
+}
+
+// 1 / sqrt(a): the instruction's estimate (2^-26 or better) and two Newton steps.
+__device__ __forceinline__ double inverse_sqrt(double a) {
+    double r = __builtin_amdgcn_rsq(a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(r * 0.5, fma(-a * r, r, 1.), r);
+    return a < __builtin_huge_val() ? r : a == a ? 0. : a;
 }
 
 // The least e with |y| <= 7 2^e, from the bits of a finite |y|.
@@ -68,14 +95,93 @@ __device__ __forceinline__ int exponent_for(double y) {
     return min(max(k - 2 + (above ? 1 : 0), kQ4Least), kQ4Most);
 }
 
-// |t| rounded to the nearest of the 8 sizes (ties to the even code), as a code.
-__device__ __forceinline__ uint32_t code_of(double t) {
-    const double a = fabs(t);
-    const double step = a < 2. ? 0.5 : a < 4. ? 1. : 2.;
-    const double r = fmin(rint(a / step) * step, 6.);   // (steps are powers of two: exact)
-    const float f = float(r);
-    const uint32_t c = uint32_t(f < 2.f ? 2.f * f : f < 4.f ? f + 2.f : 0.5f * f + 4.f);
-    return c | (t < 0. && c ? 8u : 0u);
+// t in 32 bits, rounded so that rounding it again to a few bits gives what
+// rounding t would: towards zero, with the last bit set where that is inexact.
+__device__ __forceinline__ float to_odd(double t) {
+    const float f = float(t);
+    const double d = double(f);
+    uint32_t u = __float_as_uint(f);
+    if (fabs(d) > fabs(t)) --u;
+    if (d != t) u |= 1;
+    return __uint_as_float(u);
+}
+
+// The largest of a group's lanes.
+__device__ __forceinline__ int group_max(int e) {
+    e = max(e, __builtin_amdgcn_update_dpp(0, e, 0xB1, 0xF, 0xF, false));
+    return max(e, __builtin_amdgcn_update_dpp(0, e, 0x4E, 0xF, 0xF, false));
+}
+
+// Eight values as codes (ties to the even code, what is above 6 to 6; zero has no sign).
+__device__ __forceinline__ uint32_t codes_of(const float* t) {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[0], t[1], 1.f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[2], t[3], 1.f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[4], t[5], 1.f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[6], t[7], 1.f, 3);
+    return c & (((c | c >> 1 | c >> 2) & 0x11111111u) << 3 | 0x77777777u);
+}
+
+// A lane's eight values of a row, quantised: codes and scale byte.
+struct Quantised {
+    uint32_t codes, scale;
+};
+
+// From 64 bits.
+__device__ __forceinline__ Quantised quantise(const double* y) {
+    double most = 0.;
+    uint32_t high = 0;   // the largest exponent field, infinities and NaN included
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        most = fmax(most, fabs(y[i]));
+        high = max(high, uint32_t(__builtin_bit_cast(uint64_t, y[i]) >> 32) & 0x7fffffffu);
+    }
+    const int e = group_max(high >= 0x7ff00000u ? kQ4Most + 1 : exponent_for(most));
+    if (e > kQ4Most) return {0, kQ4Bad};
+    const double unit = __builtin_bit_cast(double, uint64_t(1023 - e) << 52);   // 2^-e
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = to_odd(y[i] * unit);
+    return {codes_of(t), uint32_t(e + 127)};
+}
+
+// The norm in 32 bits, off by less than 2^-20 (eight products and six sums of
+// positive terms in the mean, half of that in its root, the root's own 2^-23,
+// three more roundings).  False where that may leave another code or scale:
+// where values 2^-17 smaller and larger do not agree, or out of the ordinary range.
+__device__ __forceinline__ bool quantise_normed(const float* x, const f32x4* wt, float eps, Quantised& q) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = dpp_sum16(ss);
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(ss), __float_as_uint(ss), false, false);
+    ss = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(ss), __float_as_uint(ss), false, false);
+    ss = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const float inv = __builtin_amdgcn_rsqf(fmaf(ss, 1.f / kMlaLatent, eps));
+    float y[8], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = x[i] * inv * wt[i >> 2][i & 3];
+        most = fmaxf(most, fabsf(y[i]));
+    }
+    constexpr float kLess = 1.f - 0x1p-17f, kMore = 1.f + 0x1p-17f;
+    auto exponent = [](float z) {   // as exponent_for
+        const uint32_t u = __float_as_uint(z);
+        return int(u >> 23) - 129 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    };
+    const int lo = group_max(exponent(most * kLess)), hi = group_max(exponent(most * kMore));
+    const float unit = __uint_as_float(uint32_t(127 - hi) << 23);
+    float a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = y[i] * unit;
+        a[i] = t * kLess;
+        b[i] = t * kMore;
+    }
+    q = {codes_of(a), uint32_t(hi + 127)};
+    // (a group of zeros beside others is left to the other form, like every extreme)
+    return ss > 0x1p-60f && ss < 0x1p100f && hi > -60 && hi < 60 && lo == hi && q.codes == codes_of(b);
 }
 
 // A wave a row: eight latent values a lane, a group is four lanes.
@@ -95,40 +201,29 @@ __global__ __launch_bounds__(64 * kWaves) void mla_append_q4_kernel(const MlaRow
     bool packed;
     unsigned char* const out = row_at(A, t, l, packed);
     if (!out) return;
-    double y[8];
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        y[2 * i] = double(__uint_as_float(lat[i] << 16));
-        y[2 * i + 1] = double(__uint_as_float(lat[i] & 0xffff0000u));
+        v[2 * i] = __uint_as_float(lat[i] << 16);
+        v[2 * i + 1] = __uint_as_float(lat[i] & 0xffff0000u);
     }
-    if (A.weight) {
-        double ss = 0.;
+    Quantised q;
+    if (!A.weight || !__all(quantise_normed(v, wt, A.eps, q))) {
+        double y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fma(y[i], y[i], ss);
+        for (int i = 0; i < 8; ++i) y[i] = double(v[i]);
+        if (A.weight) {
+            double ss = 0.;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) ss += shuffle_xor(ss, d);
-        const double rms = sqrt(ss * (1. / kMlaLatent) + double(A.eps));
-        const double inv = 1. / rms;
+            for (int i = 0; i < 8; ++i) ss = fma(y[i], y[i], ss);
+            const double inv = inverse_sqrt(wave_sum(ss) * (1. / kMlaLatent) + double(A.eps));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * double(wt[i >> 2][i & 3]);
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * double(wt[i >> 2][i & 3]);
+        }
+        q = quantise(y);
     }
-    double most = 0.;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        most = fmax(most, fabs(y[i]));
-        bad |= !(fabs(y[i]) < __builtin_huge_val());
-    }
-    int e = bad ? kQ4Most + 1 : exponent_for(most);
-    e = max(e, __shfl_xor(e, 1));
-    e = max(e, __shfl_xor(e, 2));
-    bad = e > kQ4Most;
-    uint32_t codes = 0;
-    const double unit = __builtin_bit_cast(double, uint64_t(1023 - e) << 52);   // 2^-e
-#pragma unroll
-    for (int i = 0; i < 8; ++i) codes |= code_of(y[i] * unit) << (4 * i);
-    *reinterpret_cast<uint32_t*>(out + 4 * l) = bad ? 0u : codes;
-    if ((l & 3) == 0) out[kQ4ScaleAt + l / 4] = static_cast<unsigned char>(bad ? kQ4Bad : uint32_t(e + 127));
+    *reinterpret_cast<uint32_t*>(out + 4 * l) = q.codes;
+    if ((l & 3) == 0) out[kQ4ScaleAt + l / 4] = static_cast<unsigned char>(q.scale);
     if (l < 8) *reinterpret_cast<u32x4*>(out + kQ4PeAt + 16 * l) = pe;
 }
 
