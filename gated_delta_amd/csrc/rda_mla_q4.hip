@@ -32,29 +32,42 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, 
     return lo;
 }
 
-// Where row t of the call lies in the cache: nullptr where nowhere.
-// `packed` is false where t belongs to no sequence.
-__device__ __forceinline__ unsigned char* row_at(const MlaRowsQ4Args& A, int t, int l, bool& packed) {
-    int seq, place, fresh;
-    if (A.cu) {
-        seq = find_seq(A.cu, A.num_seqs, t, l);
-        const int a = A.cu[seq];
-        place = t - a;
-        fresh = A.cu[seq + 1] - a;
-    } else {
-        fresh = A.total / A.num_seqs;
-        seq = t / fresh;
-        place = t - seq * fresh;
+// Where the kRows rows from `t` on lie in the cache, looked up by a lane each.
+struct Places {
+    uint64_t at;     // lane r: row t + r's address, 0 where it has none
+    bool packed;     // and whether it belongs to a sequence
+    template <int kRows>
+    __device__ __forceinline__ void find(const MlaRowsQ4Args& A, int t, int l) {
+        const int row = min(t + min(l, kRows - 1), A.total - 1);
+        int seq, place, fresh;
+        if (A.cu) {
+            seq = find_seq(A.cu, A.num_seqs, t, l);
+            if constexpr (kRows > 1)
+                while (seq + 1 < A.num_seqs && A.cu[seq + 1] <= row) ++seq;
+            const int a = A.cu[seq];
+            place = row - a;
+            fresh = A.cu[seq + 1] - a;
+        } else {
+            fresh = A.total / A.num_seqs;
+            seq = row / fresh;
+            place = row - seq * fresh;
+        }
+        at = 0;
+        packed = place >= 0 && place < fresh && t + l < A.total;
+        if (!packed) return;
+        const int64_t pos = int64_t(A.kv_lens[seq]) - fresh + place;
+        if (pos < 0 || pos >= (int64_t(A.table_width) << A.page_shift)) return;
+        const int page = A.table[int64_t(seq) * A.table_width + (pos >> A.page_shift)];
+        if (page < 0 || page >= A.num_pages) return;
+        at = reinterpret_cast<uint64_t>(A.cache) + uint64_t(page) * uint64_t(A.page_stride) +
+             uint64_t(pos & ((1 << A.page_shift) - 1)) * kQ4Row;
     }
-    packed = place >= 0 && place < fresh;
-    if (!packed) return nullptr;
-    const int64_t pos = int64_t(A.kv_lens[seq]) - fresh + place;
-    if (pos < 0 || pos >= (int64_t(A.table_width) << A.page_shift)) return nullptr;
-    const int page = A.table[int64_t(seq) * A.table_width + (pos >> A.page_shift)];
-    if (page < 0 || page >= A.num_pages) return nullptr;
-    return A.cache + int64_t(page) * A.page_stride +
-           int64_t(pos & ((1 << A.page_shift) - 1)) * kQ4Row;
-}
+    __device__ __forceinline__ unsigned char* row(int r) const {
+        return reinterpret_cast<unsigned char*>(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(at >> 32), r))) << 32 |
+                                                uint32_t(__builtin_amdgcn_readlane(int(at), r)));
+    }
+    __device__ __forceinline__ bool in_sequence(int r) const { return __ballot(packed) >> r & 1; }
+};
 
 // x + the values of the other lanes of the wavefront.
 __device__ __forceinline__ double wave_sum(double x) {
@@ -112,13 +125,16 @@ __device__ __forceinline__ int group_max(int e) {
     return max(e, __builtin_amdgcn_update_dpp(0, e, 0x4E, 0xF, 0xF, false));
 }
 
-// Eight values as codes (ties to the even code, what is above 6 to 6; zero has no sign).
+// Eight values as codes (ties to the even code, what is above 6 to 6), and the same
+// where zero has no sign.
 __device__ __forceinline__ uint32_t codes_of(const float* t) {
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[0], t[1], 1.f, 0);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[2], t[3], 1.f, 1);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[4], t[5], 1.f, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[6], t[7], 1.f, 3);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[6], t[7], 1.f, 3);
+}
+__device__ __forceinline__ uint32_t without_minus_zero(uint32_t c) {
     return c & (((c | c >> 1 | c >> 2) & 0x11111111u) << 3 | 0x77777777u);
 }
 
@@ -142,49 +158,50 @@ __device__ __forceinline__ Quantised quantise(const double* y) {
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = to_odd(y[i] * unit);
-    return {codes_of(t), uint32_t(e + 127)};
+    return {without_minus_zero(codes_of(t)), uint32_t(e + 127)};
 }
 
 // The norm in 32 bits, off by less than 2^-20 (eight products and six sums of
 // positive terms in the mean, half of that in its root, the root's own 2^-23,
-// three more roundings).  False where that may leave another code or scale:
+// five more roundings).  False where that may leave another code or scale:
 // where values 2^-17 smaller and larger do not agree, or out of the ordinary range.
 __device__ __forceinline__ bool quantise_normed(const float* x, const f32x4* wt, float eps, Quantised& q) {
-    float ss = 0.f;
+    float ss = 0.f, y[8], most = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 8; ++i) {
+        ss = fmaf(x[i], x[i], ss);
+        y[i] = x[i] * wt[i >> 2][i & 3];
+        most = fmaxf(most, fabsf(y[i]));
+    }
     ss = dpp_sum16(ss);
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(ss), __float_as_uint(ss), false, false);
     ss = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(ss), __float_as_uint(ss), false, false);
     ss = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     const float inv = __builtin_amdgcn_rsqf(fmaf(ss, 1.f / kMlaLatent, eps));
-    float y[8], most = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = x[i] * inv * wt[i >> 2][i & 3];
-        most = fmaxf(most, fabsf(y[i]));
-    }
-    constexpr float kLess = 1.f - 0x1p-17f, kMore = 1.f + 0x1p-17f;
+    const float less = inv * (1.f - 0x1p-17f), more = inv * (1.f + 0x1p-17f);
     auto exponent = [](float z) {   // as exponent_for
         const uint32_t u = __float_as_uint(z);
         return int(u >> 23) - 129 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     };
-    const int lo = group_max(exponent(most * kLess)), hi = group_max(exponent(most * kMore));
-    const float unit = __uint_as_float(uint32_t(127 - hi) << 23);
+    const int lo = group_max(exponent(most * less)), hi = group_max(exponent(most * more));
+    const float unit = __uint_as_float(uint32_t(127 - hi) << 23), small = less * unit, large = more * unit;
     float a[8], b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = y[i] * unit;
-        a[i] = t * kLess;
-        b[i] = t * kMore;
+        a[i] = y[i] * small;
+        b[i] = y[i] * large;
     }
-    q = {codes_of(a), uint32_t(hi + 127)};
+    const uint32_t codes = codes_of(a);
+    q = {without_minus_zero(codes), uint32_t(hi + 127)};
     // (a group of zeros beside others is left to the other form, like every extreme)
-    return ss > 0x1p-60f && ss < 0x1p100f && hi > -60 && hi < 60 && lo == hi && q.codes == codes_of(b);
+    return ss > 0x1p-60f && ss < 0x1p100f && most > 0x1p-60f && most < 0x1p60f && hi > -60 && hi < 60 && lo == hi &&
+           codes == codes_of(b);
 }
 
-// A wave a row: eight latent values a lane, a group is four lanes.
+// A wave a row: eight latent values a lane, a group is four lanes.  (Bound by the
+// arithmetic: several rows a wave take longer, 15.8 us with two and 18.4 with four
+// for 14.5.)
 __global__ __launch_bounds__(64 * kWaves) void mla_append_q4_kernel(const MlaRowsQ4Args A) {
     const int l = threadIdx.x & 63;
     const int t = blockIdx.x * kWaves + wave_id();
@@ -198,8 +215,9 @@ __global__ __launch_bounds__(64 * kWaves) void mla_append_q4_kernel(const MlaRow
         wt[0] = *reinterpret_cast<const f32x4*>(A.weight + 8 * l);
         wt[1] = *reinterpret_cast<const f32x4*>(A.weight + 8 * l + 4);
     }
-    bool packed;
-    unsigned char* const out = row_at(A, t, l, packed);
+    Places P;
+    P.find<1>(A, t, l);
+    unsigned char* const out = P.row(0);
     if (!out) return;
     float v[8];
 #pragma unroll
@@ -227,38 +245,54 @@ __global__ __launch_bounds__(64 * kWaves) void mla_append_q4_kernel(const MlaRow
     if (l < 8) *reinterpret_cast<u32x4*>(out + kQ4PeAt + 16 * l) = pe;
 }
 
-// A wave a row: eight latent values a lane.
+// kRows rows a wave: eight latent values a lane.
+template <int kRows>
 __global__ __launch_bounds__(64 * kWaves) void mla_read_q4_kernel(const MlaRowsQ4Args A) {
     const int l = threadIdx.x & 63;
-    const int t = blockIdx.x * kWaves + wave_id();
+    const int t = (blockIdx.x * kWaves + wave_id()) * kRows;
     if (t >= A.total) return;
-    bool packed;
-    const unsigned char* const row = row_at(A, t, l, packed);
-    if (!packed) return;
-    u32x4 y = {}, pe = {};
-    if (row) {
-        const uint32_t codes = *reinterpret_cast<const uint32_t*>(row + 4 * l);
-        const uint32_t s = row[kQ4ScaleAt + l / 4];
-        if (l < 8) pe = *reinterpret_cast<const u32x4*>(row + kQ4PeAt + 16 * l);
-        y = q4_eight(codes, q4_scale(s));
-        if (s == kQ4Bad) y = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+    Places P;
+    P.find<kRows>(A, t, l);
+    uint32_t codes[kRows], scale[kRows];
+    u32x4 pe[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const unsigned char* const row = P.row(r);
+        codes[r] = 0;
+        scale[r] = 1;
+        pe[r] = u32x4{};
+        if (!row) continue;
+        codes[r] = *reinterpret_cast<const uint32_t*>(row + 4 * l);
+        scale[r] = row[kQ4ScaleAt + l / 4];
+        if (l < 8) pe[r] = *reinterpret_cast<const u32x4*>(row + kQ4PeAt + 16 * l);
     }
-    uint16_t* const out = A.out + int64_t(t) * A.out_stride;
-    *reinterpret_cast<u32x4*>(out + 8 * l) = y;
-    if (l < 8) *reinterpret_cast<u32x4*>(out + kMlaLatent + 8 * l) = pe;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (!P.in_sequence(r)) continue;
+        u32x4 y = q4_eight(codes[r], q4_scale(scale[r]));
+        if (scale[r] == kQ4Bad) y = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+        uint16_t* const out = A.out + int64_t(t + r) * A.out_stride;
+        *reinterpret_cast<u32x4*>(out + 8 * l) = y;
+        if (l < 8) *reinterpret_cast<u32x4*>(out + kMlaLatent + 8 * l) = pe[r];
+    }
 }
 
-unsigned grid(const MlaRowsQ4Args& A) { return unsigned((A.total + kWaves - 1) / kWaves); }
+unsigned grid(const MlaRowsQ4Args& A, int rows) {
+    return unsigned((A.total + kWaves * rows - 1) / (kWaves * rows));
+}
 
 }  // namespace
 
 hipError_t launch_mla_append_q4(const MlaRowsQ4Args& A, hipStream_t stream) {
-    mla_append_q4_kernel<<<dim3(grid(A)), dim3(64 * kWaves), 0, stream>>>(A);
+    mla_append_q4_kernel<<<dim3(grid(A, 1)), dim3(64 * kWaves), 0, stream>>>(A);
     return hipGetLastError();
 }
 
 hipError_t launch_mla_read_q4(const MlaRowsQ4Args& A, hipStream_t stream) {
-    mla_read_q4_kernel<<<dim3(grid(A)), dim3(64 * kWaves), 0, stream>>>(A);
+    // two rows a wave where there are waves enough (32768 rows 11.1 us for 12.2 with
+    // one and 12.6 with four)
+    if (A.total >= 8192) mla_read_q4_kernel<2><<<dim3(grid(A, 2)), dim3(64 * kWaves), 0, stream>>>(A);
+    else mla_read_q4_kernel<1><<<dim3(grid(A, 1)), dim3(64 * kWaves), 0, stream>>>(A);
     return hipGetLastError();
 }
 
