@@ -560,9 +560,9 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
     int per = max((total + workgroups - 1) / workgroups, A.min_tiles);
     // Where the workgroups suffice for it none goes on to another unit: the units'
     // tiles are counted up to multiples of a share then, one as large as that line's
-    // at most.
+    // at most.  (Their sums are below four times the tiles' number.)
     bool apart = false;
-    if (units <= workgroups && A.batch <= kThreads) {
+    if (units <= workgroups && A.batch <= kThreads && total < 1 << 28) {
         int most = n0, tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
@@ -594,7 +594,7 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
         }
     }
     if (int64_t(per) * wg >= total) return;
-    const int begin = per * wg, end = min(begin + per, total);
+    const int begin = per * wg, end = begin + min(per, total - begin);
     for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
         const int b = b0 + int(threadIdx.x);
         int x = x0, before = before0, sum = total0;
@@ -656,7 +656,7 @@ __device__ __forceinline__ void walk_prefix(const MlaDecodeArgs& A, Lds<kRW>& ld
     const int n = tiles_of(A.prefix_len);
     const int total = A.prefix_units * n;
     int at = A.prefix_per * wg;
-    const int end = min(at + A.prefix_per, total);
+    const int end = at + min(A.prefix_per, total - at);
     int turn = 1;
     while (at < end) {
         const int unit = at / n, first = at - unit * n;

@@ -26,7 +26,8 @@
  * inputs from the raw projections (short convolution, q/k norm, gates), and
  * rda_output_norm_gate is the block's output norm and gate on the mixer's
  * output.  The layers between the mixer's have rda_mla_prefill, rda_mla_decode
- * and rda_mla_append (latent attention and its paged cache), and
+ * and rda_mla_append (latent attention and its paged cache; with the cache in 4
+ * bits rda_mla_decode_q4, rda_mla_append_q4 and rda_mla_read_q4), and
  * rda_verify_drafts yields the accept counts that rda_decode_tokens takes.
  *
  * Conventions shared by every entry point
@@ -611,7 +612,9 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
  *                     c / 2, an even one in the low half: 0, 0.5, 1, 1.5, 2,
  *                     3, 4, 6 for the codes 0 .. 7, negative with bit 3
  *   bytes [256, 272)  a scale byte s for each 32 channels, whose values are
- *                     the codes' times 2^(s - 127); 255: all 32 are NaN
+ *                     the codes' times 2^(s - 127); 255: all 32 are NaN (s is
+ *                     in [7, 252] otherwise: other bytes are never written,
+ *                     and read as unspecified values)
  *   bytes [272, 400)  the 64 shared key channels in bf16
  *
  * and a page of page_tokens rows (as in rda_mla_decode) lies page_stride bytes
@@ -661,11 +664,13 @@ size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t 
 
 /*
  * rda_mla_decode over the 4-bit cache (page_stride in bytes; every other
- * argument, limit and error as there).  The query is used as it is: in the
- * products with the codes it is a pair of 8-bit values with scales of the
- * row's largest magnitude, together off by at most 2^-21 of that.  A query row
- * whose latent part holds an infinity or NaN, and one that sees a row with a
- * NaN group, gives NaN throughout; rows that it does not see do not reach it.
+ * argument, limit and error as there, but table_width x page_tokens at most
+ * 2^31 - 4096, with 192 more in the limit on the product).  The query is used
+ * as it is: in the products with the codes it is a pair of 8-bit values with
+ * scales of the row's largest magnitude, together off by at most 2^-22 of that
+ * (or 2^-118, if that is more).  A query row whose latent part holds an
+ * infinity or NaN, and one that sees a row with a NaN group, gives NaN
+ * throughout; rows that it does not see do not reach it.
  */
 rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
                              int32_t page_tokens, const int32_t* block_table, int32_t table_width,
