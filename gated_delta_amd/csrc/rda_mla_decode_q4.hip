@@ -409,6 +409,9 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
             float mn = fmaxf(m, top);
 #pragma unroll
             for (int k = 0; k < S::kKeyWaves; ++k) mn = fmaxf(mn, lds.top[k * S::kRowWaves + rw][c16]);
+            // (a row that has not outgrown its own keeps it: its result does not
+            // depend on the rows beside it)
+            if (!((mn - m) * c > 8.f)) mn = m;
             const float mun = mn == kNone ? 0.f : mn * c;
             const float a = m == kNone ? 0.f : __builtin_amdgcn_exp2f(mu - mun);
             m = mn;
