@@ -12,8 +12,9 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
-constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 4, kJoinRows = 128;
+constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 8, kJoinRows = 128;
 constexpr int kPieceTiles = 6;
+constexpr int kBothTiles = 6;
 
 // A workgroup of 32 kRW query rows: 4 kRW waves.
 template <int kRW>
@@ -227,6 +228,7 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
         const int valid = end - (tile * kTile + S::kFetchRows * w);
         const uint32_t to = tiles + (tile - t0) % kBuf * kTileBytes + w * S::kFetchRows * kQ4Row;
         if (__builtin_expect(valid >= S::kFetchRows, 1)) q4_fetch_rows<kCausal>(from, lane16, to);
+        else if (valid <= 0) q4_fetch_rows<false>(kQ4Zeros, lane16, to);
         else q4_fetch_some(from, valid, l, to);
     };
     if (S::kWaves == 4 || w < 4) find_rows();
@@ -515,6 +517,17 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     raw_barrier();   // the next piece writes what this one has read
 }
 
+// Sums of x over the lanes up to each.
+__device__ __forceinline__ int scan64(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);   // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);   // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);   // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+    return x;
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 // Workgroup `wg` of those that share out the sequences' tiles.
@@ -522,13 +535,15 @@ template <int kRW>
 __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>& lds, int wg, int workgroups) {
     constexpr int kThreads = Shape<kRW>::kThreads, kWaves = Shape<kRW>::kWaves;
     const int l = threadIdx.x & 63, w = wave_id();
+    // up to 64 sequences: every wave for itself, a lane a sequence
+    const bool few = A.batch <= 64;
+    const int lane = few ? l : int(threadIdx.x);
 
-    auto block_sum = [&](int x, int& before) {   // x over the workgroup
-        int s = x;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(s, d);
-            if (l >= d) s += y;
+    auto block_sum = [&](int x, int& before) {   // x over the lanes
+        int s = scan64(x);
+        if (few) {
+            before = s - x;
+            return __builtin_amdgcn_readlane(s, 63);
         }
         __syncthreads();
         if (l == 63) lds.scan[w] = s;
@@ -547,7 +562,7 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
     // pay anyway (queries in, sums out); a workgroup that goes on to another unit pays
     // again, as much as kPieceTiles tiles.  So the line that is cut into equal
     // shares holds that many places before each unit's tiles.
-    const int n0 = tiles_at(threadIdx.x);
+    const int n0 = tiles_at(lane);
     int head = kPieceTiles, before0;
     auto places = [&](int n) { return n > 0 ? n + head : 0; };
     int x0 = places(n0);
@@ -560,19 +575,20 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
     total *= A.row_blocks;
     if (total == 0) return;
     const int units = A.batch * A.row_blocks;
+    if (kRW == 1 && total < kBothTiles * workgroups) workgroups /= 2;
     int per = max((total + workgroups - 1) / workgroups, A.min_tiles);
     // Where the workgroups suffice for it none goes on to another unit: the units'
     // tiles are counted up to multiples of a share then, one as large as that line's
     // at most.  (Their sums are below four times the tiles' number.)
     bool apart = false;
     if (units <= workgroups && A.batch <= kThreads && total < 1 << 28) {
-        int most = n0, tiles;
+        int most = int(umax_over_quarters(dpp_umax16(uint32_t(n0)))), tiles;
+        if (!few) {
+            if (l == 0) lds.scan[kWaves + w] = most;
+            __syncthreads();
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-        if (l == 0) lds.scan[kWaves + w] = most;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
+            for (int k = 0; k < kWaves; ++k) most = max(most, lds.scan[kWaves + k]);
+        }
         most = __builtin_amdgcn_readfirstlane(most);
         {
             int before;
@@ -597,24 +613,35 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
         }
     }
     if (int64_t(per) * wg >= total) return;
+    int unit = 0, first = 0;
     const int begin = per * wg, end = begin + min(per, total - begin);
     for (int b0 = 0, seen = 0; b0 < A.batch && seen * A.row_blocks <= begin; b0 += kThreads) {
-        const int b = b0 + int(threadIdx.x);
+        const int b = b0 + lane;
         int x = x0, before = before0, sum = total0;
         if (b0 > 0) {
             x = places(tiles_at(b));
             sum = block_sum(x, before);
         }
         const int at = begin - (seen + before) * A.row_blocks;
-        if (x > 0 && at >= 0 && at < x * A.row_blocks) {
+        const bool mine = x > 0 && at >= 0 && at < x * A.row_blocks;
+        if (few) {
+            const int k = __builtin_ctzll(__ballot(mine));   // (one lane's share holds `begin`)
+            const int n = __builtin_amdgcn_readlane(x, k), in = __builtin_amdgcn_readlane(at, k);
+            unit = k * A.row_blocks + in / n;
+            first = in % n;
+        } else if (mine) {
             lds.unit = b * A.row_blocks + at / x;
             lds.first = at % x;
         }
         seen += sum;
     }
-    __syncthreads();
-    int unit = __builtin_amdgcn_readfirstlane(lds.unit);
-    int first = __builtin_amdgcn_readfirstlane(lds.first);
+    if (!few) {
+        __syncthreads();
+        unit = lds.unit;
+        first = lds.first;
+    }
+    unit = __builtin_amdgcn_readfirstlane(unit);
+    first = __builtin_amdgcn_readfirstlane(first);
 
     const int unit_rows = A.tokens * A.heads;
     int at = begin, turn = 1;   // (turn: a number for each tile, for lds.moved)
@@ -794,29 +821,29 @@ __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDeco
 }
 
 // The same for few rows, which may have hundreds of pieces each: a workgroup per
-// row and 128 channels, whose 16 waves share out the pieces.
+// row and 64 channels, whose 32 half-waves share out the pieces.
 __global__ __launch_bounds__(kJoinWide) void mla_join_wide_q4_kernel(const MlaDecodeArgs A) {
-    constexpr int kWaves = kJoinWide / 64;
-    __shared__ float ml[kWaves][2];
-    __shared__ f32x2 sums[kWaves][64];
-    const int l = threadIdx.x & 63, w = wave_id();
+    constexpr int kParts = kJoinWide / 32;
+    __shared__ float ml[kParts][2];
+    __shared__ f32x2 sums[kParts][32];
+    const int l = threadIdx.x & 31, part = threadIdx.x / 32;
     const int row = blockIdx.x / kJoinSlices, ch = blockIdx.x % kJoinSlices * (kMlaLatent / kJoinSlices) + 2 * l;
     Pieces P;
-    if (!P.find(A, row)) return;   // (the same for all waves)
+    if (!P.find(A, row)) return;   // (the same for all)
     Joined<2> J;
-    J.add(A, P, w, kWaves, ch);
+    J.add(A, P, part, kParts, ch);
     if (l == 0) {
-        ml[w][0] = J.top;
-        ml[w][1] = J.total;
+        ml[part][0] = J.top;
+        ml[part][1] = J.total;
     }
-    sums[w][l] = J.sum;
+    sums[part][l] = J.sum;
     __syncthreads();
-    if (w > 0) return;
-    const int waves = min(kWaves, P.n);
-    for (int k = 1; k < waves; ++k) J.top = fmaxf(J.top, ml[k][0]);
+    if (part > 0) return;
+    const int parts = min(kParts, P.n);
+    for (int k = 1; k < parts; ++k) J.top = fmaxf(J.top, ml[k][0]);
     J.total = 0.f;
     J.sum = 0.f;
-    for (int k = 0; k < waves; ++k) J.take(ml[k][0], ml[k][1], sums[k][l]);
+    for (int k = 0; k < parts; ++k) J.take(ml[k][0], ml[k][1], sums[k][l]);
     J.put(A, row, ch, ch == 0);
 }
 

@@ -121,7 +121,8 @@ __device__ __forceinline__ void q4_fetch_rows(const void* rows, uint32_t lane16,
 }
 
 // The same where only the first `valid` rows are to be read: the others become zeros.
-__device__ const __attribute__((aligned(16))) uint32_t kQ4Zeros[4] = {};
+// (eight rows of zeros: what a tile behind the last one is filled from)
+__device__ const __attribute__((aligned(16))) uint32_t kQ4Zeros[8 * kQ4Row / 4] = {};
 
 __device__ __forceinline__ void q4_fetch_some(const char* rows, int valid, int lane, uint32_t lds) {
     const char* const zeros = reinterpret_cast<const char*>(kQ4Zeros);
