@@ -95,6 +95,8 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // sums (64 KiB per 32 rows) than in tiles (36 KiB each).  2 instead of 4: 8 x
 // 270 rows x 80 query rows 26 us for 28, but 7 sequences of 950 rows 22.5 for
 // 20.5 and one of 777 rows 21 for 20.
+// Over the 4-bit cache (q4) blocks are of 32 or 64 rows, and 2 tiles are the least:
+// one sequence of 777 rows 19.7 us for 21.1.
 size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     const int64_t unit_rows = int64_t(A.tokens) * A.heads, rows = unit_rows * A.batch;
     const int most_waves = q4 ? 2 : 4, workgroups = q4 ? kQ4Workgroups : kMlaWorkgroups;
@@ -109,7 +111,7 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     };
     const size_t units = size_t(A.batch) * A.row_blocks;
     A.meta = reinterpret_cast<int32_t*>(take(units * 2 * sizeof(int32_t)));
-    A.bad = reinterpret_cast<int32_t*>(take((units + workgroups) * sizeof(int32_t)));
+    if (!q4) A.bad = reinterpret_cast<int32_t*>(take((units + workgroups) * sizeof(int32_t)));
     const size_t slots = (units + workgroups) * 32 * A.row_waves;
     A.part = reinterpret_cast<float*>(take(slots * RDA_MLA_LATENT * sizeof(float)));
     A.part_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
@@ -117,7 +119,7 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     A.prefix_units = 0;
     A.prefix_per = 1;
     if (A.prefix_len > 0 && rows > 0) {
-        // blocks of 128 rows once they fill the chip with long shares, or half of it
+        // blocks of 128 rows (q4: 64) once they fill the chip with long shares, or half of it
         // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
         // blocks of 32, whose four waves share out the tiles
         const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
@@ -127,8 +129,9 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
         const int64_t share = (A.prefix_units * tiles + workgroups - 1) / workgroups;
         const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
         A.prefix_per = int32_t(share > least ? share : least);
-        A.pre_bad = reinterpret_cast<int32_t*>(
-            take((size_t(A.prefix_units) + workgroups) * sizeof(int32_t)));
+        if (!q4)
+            A.pre_bad = reinterpret_cast<int32_t*>(
+                take((size_t(A.prefix_units) + workgroups) * sizeof(int32_t)));
         const size_t ps = (size_t(A.prefix_units) + workgroups) * 32 * A.prefix_waves;
         A.pre_part = reinterpret_cast<float*>(take(ps * RDA_MLA_LATENT * sizeof(float)));
         A.pre_ml = reinterpret_cast<float*>(take(ps * 2 * sizeof(float)));

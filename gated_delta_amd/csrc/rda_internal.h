@@ -378,7 +378,6 @@ hipError_t launch_mla_append(const MlaAppendArgs& A, hipStream_t stream);
 
 // The same over a cache of 4-bit rows: MlaDecodeArgs with cache the pages'
 // bytes and page_stride in bytes.
-constexpr int kQ4Tile = 32;           // cached rows per tile
 constexpr int kQ4Workgroups = 512;    // of 32 query rows: two per CU; of 64 half as many
 hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream);
 

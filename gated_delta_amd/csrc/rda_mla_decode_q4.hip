@@ -1,5 +1,48 @@
 // rda_mla_decode_q4.hip -- absorbed latent attention over a paged latent cache
-// in 4 bits.
+// in 4 bits: for a query row q and the cached rows c_j that it sees,
+//   s_j = scale q . c_j,  m = some reference,  p_j = exp(s_j - m),
+//   o = sum_j p_j c_j[0:512] / sum_j p_j,  lse = m + log sum_j p_j.
+//
+// A cached row is 400 bytes and is read once for 32 or 64 query rows, so one
+// token of 32 heads is a matter of bytes, several tokens or a prefix that all
+// share one of products (2176 flop a cached row and query row).
+//
+// Scores.  The codes enter the matrix instruction as they lie in LDS: it takes
+// 4-bit operands with a scale byte per 32 values, and a 16-byte granule is one
+// lane's share.  Its other operand has 8 bits at most, so a query is hi + lo, each
+// e4m3 with one scale a row: 4 + 4 significant bits, as many as bf16 has.  The two
+// products cost what one of bf16 over unpacked rows would, and nothing is unpacked
+// for them.  The 64 shared channels are bf16 products.
+// Values.  Probabilities are rounded to bf16 (once, off by 2^-8 at most) and the
+// codes unpacked to bf16 (exact; each value once a workgroup, into its wave's own
+// LDS), since the product runs over rows and scales go with channels: the probability
+// would have to carry every group's scale.  Sums O^T, 32 channels by 32 query rows
+// a block, stay in placed accumulation registers.
+// Softmax.  The reference of a row moves only when the row outgrows it by 2^8, so
+// the sums are hardly ever rescaled; scores, probabilities' sums and outputs are
+// held in fp32.
+//
+// A workgroup has a wave per 16 query rows and half a tile of 32 cached rows for the
+// scores, and each wave sums 128 or 64 channels of all its query rows.  Tile
+// i + 1's scores run beside tile i's values, with one barrier a tile.  Tiles come by
+// LDS-DMA in a ring of 4 or 8; their addresses are looked up 64 tiles at a time, one a
+// lane.  The tiles of all sequences are one line that is cut into equal shares on
+// the device (walk_sequences), and what is cut is joined by a second kernel.
+//
+// Bound by: the waits between those stages.  Of 3700 cycles for two tiles of a CU's
+// two workgroups 1090 are matrix instructions and 1650 LDS transfers (an unpacked
+// granule costs 13 cycles to write and 2 a row to read transposed).
+//   256 sequences of 512 to 8192 rows, 32 query rows: 141 us of which the joining takes
+//     10; 445 MB, 3.2 TB/s (73 us at 6.1)
+//   32 of them, 96 query rows: 71 us
+//   12288 query rows behind 16384 shared rows: 480 us, 920 TFLOP/s
+//   one sequence of 131072 rows: 40 us; of 1000: 16.7
+// Not faster: values read transposed as codes with the scale as an exponent added to
+// the probability (158.6 us for the first case and 577 for the third, both 10 %
+// slower: 220 ordinary instructions a wave and tile for 160); 128 query rows a
+// workgroup with one wave a SIMD and 256 sums (32 x 3 tokens 95 us for 79);
+// half of the waves unpacking at the other end of a tile (82 for 79); sums stored
+// past the caches (160 for 156).
 #include <type_traits>
 
 #include "rda_mla_q4.h"
@@ -12,11 +55,20 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
-constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 8, kJoinRows = 128;
+constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 8;
+// Up to as many query rows are joined by a workgroup per row and slice: one sequence
+// of 131072 rows 48 us for 117.  More rows than that fill the chip with a wave each.
+constexpr int kJoinRows = 128;
+// What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us).
 constexpr int kPieceTiles = 6;
+// Shares of fewer tiles than this for two workgroups a CU are made twice as long for
+// one: half the pieces to write and join, but no second workgroup to fill a tile's
+// waits.  65536 rows (4 tiles) 32.6 us for 35.7, 16 x 2048 27.4 for 31.8; 131072 (8)
+// 41.8 either way; 64 of 1000 and 3000 rows (8) 42.3 for 39.5.
 constexpr int kBothTiles = 6;
 
-// A workgroup of 32 kRW query rows: 4 kRW waves.
+// A workgroup of 32 kRW query rows: 4 kRW waves.  One of 32 rows leaves room for a
+// second on its CU; one of 64 reads a tile once for twice the rows.
 template <int kRW>
 struct Shape {
     static constexpr int kWaves = 4 * kRW, kThreads = 64 * kWaves;
@@ -392,9 +444,12 @@ __device__ __forceinline__ void piece(const MlaDecodeArgs& A, Lds<kRW>& lds, con
     const int n_tiles = t1 - t0;
 #pragma unroll 1
     for (int i = 0; i < n_tiles; ++i) {
-        // (two workgroups of a CU take turns: left alone the older one goes first)
-        if ((i ^ (blockIdx.x >> 8)) & 1) __builtin_amdgcn_s_setprio(1);
-        else __builtin_amdgcn_s_setprio(0);
+        // (two workgroups of a CU take turns: left alone the older one goes first, and
+        // the younger ends 23 of 108 us later)
+        if constexpr (kRW == 1) {
+            if ((i ^ (blockIdx.x >> 8)) & 1) __builtin_amdgcn_s_setprio(1);
+            else __builtin_amdgcn_s_setprio(0);
+        }
         wait_vm<(kBuf - 3) * kQ4Fetch>();   // this wave's part of the next tile
         raw_barrier();                      // everyone's; the tile before is read
         const uint32_t next = tiles + ((i + 1) % kBuf) * kTileBytes;
@@ -809,7 +864,8 @@ struct Joined {
     }
 };
 
-// Joins the partial sums of a query row, a wave per row.
+// Joins the partial sums of a query row, a wave per row: 8192 rows of about three
+// pieces 10 us.
 __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDecodeArgs A) {
     const int l = threadIdx.x & 63;
     const int row = blockIdx.x * (kJoinThreads / 64) + wave_id();
@@ -821,7 +877,8 @@ __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDeco
 }
 
 // The same for few rows, which may have hundreds of pieces each: a workgroup per
-// row and 64 channels, whose 32 half-waves share out the pieces.
+// row and 64 channels, whose 32 half-waves share out the pieces (16 waves with 128
+// channels: 3 us more for 32 rows of 456 pieces, two more rounds of loads).
 __global__ __launch_bounds__(kJoinWide) void mla_join_wide_q4_kernel(const MlaDecodeArgs A) {
     constexpr int kParts = kJoinWide / 32;
     __shared__ float ml[kParts][2];
