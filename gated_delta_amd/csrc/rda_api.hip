@@ -126,9 +126,19 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
         const int64_t blocks = (rows + 32 * most_waves - 1) / (32 * most_waves);
         A.prefix_waves = blocks * tiles >= 8 * workgroups || 2 * blocks >= workgroups ? most_waves : 1;
         A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
-        const int64_t share = (A.prefix_units * tiles + workgroups - 1) / workgroups;
-        const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
+        const int prefix_groups = q4 ? workgroups / A.prefix_waves : workgroups;
+        const int64_t share = (A.prefix_units * tiles + prefix_groups - 1) / prefix_groups;
+        int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
+        if (q4 && rows <= kQ4WideJoin && least > 3) least = 3;
         A.prefix_per = int32_t(share > least ? share : least);
+        A.prefix_line = int32_t(tiles);
+        if (q4) {
+            const int64_t pieces = (tiles + A.prefix_per - 1) / A.prefix_per;
+            if (A.prefix_units * pieces <= prefix_groups) {
+                A.prefix_per = int32_t((tiles + pieces - 1) / pieces);
+                A.prefix_line = int32_t(A.prefix_per * pieces);
+            }
+        }
         if (!q4)
             A.pre_bad = reinterpret_cast<int32_t*>(
                 take((size_t(A.prefix_units) + workgroups) * sizeof(int32_t)));

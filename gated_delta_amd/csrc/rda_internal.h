@@ -353,6 +353,7 @@ struct MlaDecodeArgs {
     int32_t row_waves, row_blocks, min_tiles;
     int32_t prefix_waves, prefix_units;
     int32_t prefix_per;          // prefix tiles per workgroup
+    int32_t prefix_line;         // (q4) places of a block's tiles on the line that is shared out
     // workspace
     int32_t* meta;               // per unit: first and last workgroup, or -1
     int32_t *bad, *pre_bad;      // per slot of partial sums
@@ -379,6 +380,7 @@ hipError_t launch_mla_append(const MlaAppendArgs& A, hipStream_t stream);
 // The same over a cache of 4-bit rows: MlaDecodeArgs with cache the pages'
 // bytes and page_stride in bytes.
 constexpr int kQ4Workgroups = 512;    // of 32 query rows: two per CU; of 64 half as many
+constexpr int kQ4WideJoin = 128;      // query rows that are joined by many waves each
 hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream);
 
 // Rows into the 4-bit cache (kv, weight, eps) or out of it (out).

@@ -58,7 +58,7 @@ constexpr int kTileBytes = kTile * kQ4Row;       // 12800
 constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 8;
 // Up to as many query rows are joined by a workgroup per row and slice: one sequence
 // of 131072 rows 48 us for 117.  More rows than that fill the chip with a wave each.
-constexpr int kJoinRows = 128;
+constexpr int kJoinRows = kQ4WideJoin;
 // What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us).
 constexpr int kPieceTiles = 6;
 // Shares of fewer tiles than this for two workgroups a CU are made twice as long for
@@ -738,14 +738,14 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
 template <int kRW>
 __device__ __forceinline__ void walk_prefix(const MlaDecodeArgs& A, Lds<kRW>& lds, int wg) {
     const int rows = A.batch * A.tokens * A.heads;
-    const int n = tiles_of(A.prefix_len);
-    const int total = A.prefix_units * n;
+    const int n = tiles_of(A.prefix_len), line = A.prefix_line;   // (its last line - n are none)
+    const int total = A.prefix_units * line;
     int at = A.prefix_per * wg;
     const int end = at + min(A.prefix_per, total - at);
     int turn = 1;
     while (at < end) {
-        const int unit = at / n, first = at - unit * n;
-        const int last = min(first + (end - at), n);
+        const int unit = at / line, first = at - unit * line;
+        const int last = min(first + (end - at), line);
         const int slot = first == 0 ? unit : A.prefix_units + wg;
         Sink sink;
         sink.final = false;
@@ -754,7 +754,7 @@ __device__ __forceinline__ void walk_prefix(const MlaDecodeArgs& A, Lds<kRW>& ld
         sink.rows = min(32 * kRW, rows - unit * 32 * kRW);
         sink.part = A.pre_part + size_t(slot) * kMlaLatent * 32 * kRW;
         sink.ml = A.pre_ml + size_t(slot) * 2 * 32 * kRW;
-        piece<kRW, false>(A, lds, Source{A.prefix_table, A.prefix_len}, first, last, sink, turn);
+        piece<kRW, false>(A, lds, Source{A.prefix_table, A.prefix_len}, first, min(last, n), sink, turn);
         at += last - first;
     }
 }
@@ -798,8 +798,8 @@ struct Pieces {
             const int tiles = tiles_of(A.prefix_len);
             pu = row / pstride;
             pr = row - pu * pstride;
-            pg0 = pu * tiles / A.prefix_per;
-            n += (pu * tiles + tiles - 1) / A.prefix_per - pg0 + 1;
+            pg0 = pu * A.prefix_line / A.prefix_per;
+            n += (pu * A.prefix_line + tiles - 1) / A.prefix_per - pg0 + 1;
         }
         return true;
     }
@@ -907,7 +907,7 @@ __global__ __launch_bounds__(kJoinWide) void mla_join_wide_q4_kernel(const MlaDe
 // `prefix`: workgroups for the prefix in front; sequences: those of the batch behind.
 template <int kRW>
 hipError_t launch(const MlaDecodeArgs& A, bool prefix, bool sequences, hipStream_t stream) {
-    const int64_t tiles = int64_t(A.prefix_units) * ((A.prefix_len + kTile - 1) / kTile);
+    const int64_t tiles = int64_t(A.prefix_units) * A.prefix_line;
     const int groups = prefix ? int((tiles + A.prefix_per - 1) / A.prefix_per) : 0;
     mla_decode_q4_kernel<kRW><<<dim3(unsigned(groups + (sequences ? kQ4Workgroups / kRW : 0))),
                                 dim3(Shape<kRW>::kThreads), 0, stream>>>(A, groups);
