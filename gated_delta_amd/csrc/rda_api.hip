@@ -86,6 +86,35 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
     return RDA_OK;
 }
 
+// The shared prefix in rda_mla_decode_q4: which blocks of query rows, and how their
+// tiles are shared out.
+//
+// Blocks are of 64 rows where the sequences' are, so that one launch holds both (96
+// blocks of 32 tiles beside 32 sequences of 64 rows: 38.6 us for 61.5 in two), and where
+// they give long shares by themselves (4096 query rows behind 8192: 108 us for 118, but
+// 1024 behind 8192 57 for 55), else of 32.
+// Short shares leave a quarter of the workgroups to the sequences, which run beside
+// them (32 blocks of 128 tiles: 37.5 us for 44.8), and are of 8 tiles or more; of 3 where
+// the rows are few and many waves join each (one sequence behind 1000 rows 15.8 us for
+// 19.7, 8 behind 4097 31.5 for 30).  If the workgroups suffice a block is cut into equal
+// pieces of its own (64 blocks of 10 tiles 22.4 us for 30.6, 48 of 256 93 for 114).
+void prefix_plan_q4(MlaDecodeArgs& A, int64_t rows, int64_t blocks, int64_t tiles) {
+    A.prefix_waves = A.row_waves == 2 || blocks * tiles >= 32 * kQ4Workgroups ? 2 : 1;
+    A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
+    const int64_t total = A.prefix_units * tiles;
+    int groups = kQ4Workgroups / A.prefix_waves;
+    if (total < 16 * groups) groups = groups / 4 * 3;
+    const int64_t share = (total + groups - 1) / groups, few = rows <= kQ4WideJoin ? 3 : 8;
+    const int64_t least = tiles < few ? tiles : few;   // (no more than a block has)
+    A.prefix_per = int32_t(share > least ? share : least);
+    A.prefix_line = int32_t(tiles);
+    const int64_t pieces = (tiles + A.prefix_per - 1) / A.prefix_per;
+    if (A.prefix_units * pieces <= groups) {
+        A.prefix_per = int32_t((tiles + pieces - 1) / pieces);
+        A.prefix_line = int32_t(A.prefix_per * pieces);
+    }
+}
+
 // The plan of rda_mla_decode (sizes in A) and its workspace: with ws, the
 // pointers too.  Returns the bytes.
 //
@@ -119,25 +148,19 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     A.prefix_units = 0;
     A.prefix_per = 1;
     if (A.prefix_len > 0 && rows > 0) {
-        // blocks of 128 rows (q4: 64) once they fill the chip with long shares, or half of it
-        // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
-        // blocks of 32, whose four waves share out the tiles
         const int64_t tiles = (int64_t(A.prefix_len) + 31) / 32;
         const int64_t blocks = (rows + 32 * most_waves - 1) / (32 * most_waves);
-        A.prefix_waves = blocks * tiles >= 8 * workgroups || 2 * blocks >= workgroups ? most_waves : 1;
-        A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
-        const int prefix_groups = q4 ? workgroups / A.prefix_waves : workgroups;
-        const int64_t share = (A.prefix_units * tiles + prefix_groups - 1) / prefix_groups;
-        int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
-        if (q4 && rows <= kQ4WideJoin && least > 3) least = 3;
-        A.prefix_per = int32_t(share > least ? share : least);
-        A.prefix_line = int32_t(tiles);
         if (q4) {
-            const int64_t pieces = (tiles + A.prefix_per - 1) / A.prefix_per;
-            if (A.prefix_units * pieces <= prefix_groups) {
-                A.prefix_per = int32_t((tiles + pieces - 1) / pieces);
-                A.prefix_line = int32_t(A.prefix_per * pieces);
-            }
+            prefix_plan_q4(A, rows, blocks, tiles);
+        } else {
+            // blocks of 128 rows once they fill the chip with long shares, or half of it
+            // with any (184 x 8 x 40 query rows behind 60: 280 us for 320), else
+            // blocks of 32, whose four waves share out the tiles
+            A.prefix_waves = blocks * tiles >= 8 * workgroups || 2 * blocks >= workgroups ? most_waves : 1;
+            A.prefix_units = int32_t((rows + 32 * A.prefix_waves - 1) / (32 * A.prefix_waves));
+            const int64_t share = (A.prefix_units * tiles + workgroups - 1) / workgroups;
+            const int64_t least = tiles < 8 ? tiles : 8;   // (no more than a block has)
+            A.prefix_per = int32_t(share > least ? share : least);
         }
         if (!q4)
             A.pre_bad = reinterpret_cast<int32_t*>(
