@@ -484,7 +484,8 @@ class _On:
         self.index = dev.index
 
     def __enter__(self):
-        self.before = torch.cuda.current_device()
+        # (the tensors are on a device, so there is nothing left to initialise)
+        self.before = _raw_device() if _raw_stream is not None else torch.cuda.current_device()
         if self.before != self.index:
             torch.cuda.set_device(self.index)
 
@@ -493,6 +494,7 @@ class _On:
             torch.cuda.set_device(self.before)
 
 
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -514,6 +516,9 @@ def _addr(t: Optional[torch.Tensor]):
 def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """A tensor whose rows (all but the first axis) are contiguous; returns
     the distance between rows in elements."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape \
+            and t.device == device and shape[0] > 1 and t.is_contiguous():
+        return t.stride(0)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
