@@ -94,9 +94,9 @@ rda_status check_mla_decode_sizes(int32_t batch, int32_t tokens, int32_t heads, 
 // they give long shares by themselves (4096 query rows behind 8192: 108 us for 118, but
 // 1024 behind 8192 57 for 55), else of 32.
 // Short shares leave a quarter of the workgroups to the sequences, which run beside
-// them (32 blocks of 128 tiles: 37.5 us for 44.8), and are of 8 tiles or more; of 3 where
-// the rows are few and many waves join each (one sequence behind 1000 rows 15.8 us for
-// 19.7, 8 behind 4097 31.5 for 30).  If the workgroups suffice a block is cut into equal
+// them (32 blocks of 128 tiles: 37.5 us for 44.8), and are of 6 tiles or more; of 3 where
+// the rows are few and 16 waves join each (one sequence behind 1000 rows 15.4 us for
+// 18.1, but 8 behind 4097 26.7 for 23.5).  If the workgroups suffice a block is cut into equal
 // pieces of its own (64 blocks of 10 tiles 22.4 us for 30.6, 48 of 256 93 for 114).
 void prefix_plan_q4(MlaDecodeArgs& A, int64_t rows, int64_t blocks, int64_t tiles) {
     A.prefix_waves = A.row_waves == 2 || blocks * tiles >= 32 * kQ4Workgroups ? 2 : 1;
@@ -104,7 +104,7 @@ void prefix_plan_q4(MlaDecodeArgs& A, int64_t rows, int64_t blocks, int64_t tile
     const int64_t total = A.prefix_units * tiles;
     int groups = kQ4Workgroups / A.prefix_waves;
     if (total < 16 * groups) groups = groups / 4 * 3;
-    const int64_t share = (total + groups - 1) / groups, few = rows <= kQ4WideJoin ? 3 : 8;
+    const int64_t share = (total + groups - 1) / groups, few = rows <= kQ4FewRows ? 3 : 6;
     const int64_t least = tiles < few ? tiles : few;   // (no more than a block has)
     A.prefix_per = int32_t(share > least ? share : least);
     A.prefix_line = int32_t(tiles);

@@ -380,7 +380,7 @@ hipError_t launch_mla_append(const MlaAppendArgs& A, hipStream_t stream);
 // The same over a cache of 4-bit rows: MlaDecodeArgs with cache the pages'
 // bytes and page_stride in bytes.
 constexpr int kQ4Workgroups = 512;    // of 32 query rows: two per CU; of 64 half as many
-constexpr int kQ4WideJoin = 128;      // query rows that are joined by many waves each
+constexpr int kQ4FewRows = 64;        // query rows that may have hundreds of pieces each
 hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream);
 
 // Rows into the 4-bit cache (kv, weight, eps) or out of it (out).

@@ -55,10 +55,13 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
-constexpr int kJoinThreads = 256, kJoinWide = 1024, kJoinSlices = 8;
-// Up to as many query rows are joined by a workgroup per row and slice: one sequence
-// of 131072 rows 48 us for 117.  More rows than that fill the chip with a wave each.
-constexpr int kJoinRows = kQ4WideJoin;
+constexpr int kJoinThreads = 256;
+// How many waves join a query row: 16 (32 parts of 64 channels) up to the first number
+// of rows, 4 up to the second, else one.  64 rows with 256 pieces 41 us in all for 46
+// with four waves, but 128 rows 53 for 47.5 (workgroups of 1024 threads are slow to
+// start); 256 rows with 128 pieces 37 us for 43 with one wave, 512 rows with 64 pieces
+// equal, 2048 rows with 2 pieces 40 for 37.
+constexpr int kWideRows = kQ4FewRows, kFourRows = 512;
 // What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us).
 constexpr int kPieceTiles = 6;
 // Shares of fewer tiles than this for two workgroups a CU are made twice as long for
@@ -885,18 +888,19 @@ __global__ __launch_bounds__(kJoinThreads) void mla_join_q4_kernel(const MlaDeco
     J.put(A, row, 8 * l, l == 0);
 }
 
-// The same for few rows, which may have hundreds of pieces each: a workgroup per
-// row and 64 channels, whose 32 half-waves share out the pieces (16 waves with 128
-// channels: 3 us more for 32 rows of 456 pieces, two more rounds of loads).
-__global__ __launch_bounds__(kJoinWide) void mla_join_wide_q4_kernel(const MlaDecodeArgs A) {
-    constexpr int kParts = kJoinWide / 32;
+// The same by several waves a row: kParts parts of kWidth lanes share out its pieces
+// (there may be hundreds), kLane channels a lane.
+template <int kLane, int kWidth, int kParts>
+__global__ __launch_bounds__(kWidth * kParts) void mla_join_parts_q4_kernel(const MlaDecodeArgs A) {
+    typedef typename Joined<kLane>::vec vec;
+    constexpr int kSlices = kMlaLatent / (kLane * kWidth);
     __shared__ float ml[kParts][2];
-    __shared__ f32x2 sums[kParts][32];
-    const int l = threadIdx.x & 31, part = threadIdx.x / 32;
-    const int row = blockIdx.x / kJoinSlices, ch = blockIdx.x % kJoinSlices * (kMlaLatent / kJoinSlices) + 2 * l;
+    __shared__ vec sums[kParts][kWidth];
+    const int l = threadIdx.x % kWidth, part = threadIdx.x / kWidth;
+    const int row = blockIdx.x / kSlices, ch = blockIdx.x % kSlices * (kMlaLatent / kSlices) + kLane * l;
     Pieces P;
     if (!P.find(A, row)) return;   // (the same for all)
-    Joined<2> J;
+    Joined<kLane> J;
     J.add(A, P, part, kParts, ch);
     if (l == 0) {
         ml[part][0] = J.top;
@@ -933,12 +937,10 @@ hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
     if (A.prefix_len > 0 && !together)
         if (hipError_t e = go(A.prefix_waves, true, false); e != hipSuccess) return e;
     if (hipError_t e = go(A.row_waves, together, true); e != hipSuccess) return e;
-    // up to two workgroups a CU and slice
     const int rows = A.batch * A.tokens * A.heads;
-    if (rows <= kJoinRows)
-        mla_join_wide_q4_kernel<<<dim3(unsigned(rows * kJoinSlices)), dim3(kJoinWide), 0, stream>>>(A);
-    else
-        mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
+    if (rows <= kWideRows) mla_join_parts_q4_kernel<2, 32, 32><<<dim3(unsigned(rows * 8)), dim3(1024), 0, stream>>>(A);
+    else if (rows <= kFourRows) mla_join_parts_q4_kernel<8, 64, 4><<<dim3(unsigned(rows)), dim3(256), 0, stream>>>(A);
+    else mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 
