@@ -1,5 +1,5 @@
-// rda_mla_q4.h -- the latent cache in 4 bits: its row, the conversions, and the
-// transfer of 16 rows into LDS.
+// rda_mla_q4.h -- the latent cache in 4 bits: its row, the conversions, the sums and
+// products of the attention over it, and the transfer of 8 rows into LDS.
 //
 // A row of 400 bytes: 512 latent values as e2m1 codes (256 bytes, the value of
 // an even channel in the low half of its byte), a scale byte s for each 32 of

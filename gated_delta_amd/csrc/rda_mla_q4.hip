@@ -6,9 +6,13 @@
 //   e   = the least integer with max |y| <= 7 2^e over y_c's group of 32,
 //   code = y / 2^e rounded to nearest on 0, 1/2, 1, 3/2, 2, 3, 4, 6 (ties to the
 //   even code; 7 goes to 6: no value moves further than half a step).
-// y, e and the rounding are computed in 64 bits.  A step is a quarter or more of
-// a value, so a code must not depend on how a sum was ordered; and the
-// arithmetic hides behind memory.
+// y, e and the codes are as 64 bits give them: a step is a quarter or more of a
+// value, so a code must not depend on how a sum was ordered.  With a norm 32 bits
+// are tried first (quantise_normed), and decide all codes of 99 rows in 100.
+// Bound by the arithmetic: 157 ordinary instructions a row and wave, 15.3 us for
+// 32768 rows (50.8 MB, 3.3 TB/s; 33.9 us in 64 bits throughout).
+//
+// Reading is bound by memory: 65537 rows (102 MB) 18.1 us, 5.6 TB/s.
 #include <type_traits>
 
 #include "rda_mla_q4.h"
@@ -199,9 +203,8 @@ __device__ __forceinline__ bool quantise_normed(const float* x, const f32x4* wt,
            codes == codes_of(b);
 }
 
-// A wave a row: eight latent values a lane, a group is four lanes.  (Bound by the
-// arithmetic: several rows a wave take longer, 15.8 us with two and 18.4 with four
-// for 14.5.)
+// A wave a row: eight latent values a lane, a group is four lanes.  (Several rows a
+// wave take longer, 15.8 us with two and 18.4 with four for 14.5.)
 __global__ __launch_bounds__(64 * kWaves) void mla_append_q4_kernel(const MlaRowsQ4Args A) {
     const int l = threadIdx.x & 63;
     const int t = blockIdx.x * kWaves + wave_id();
