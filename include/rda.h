@@ -630,7 +630,8 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
  *
  * where y, e and the rounding are computed in 64 bits.  No value moves further
  * than half a step between neighbouring codes of its group.  32 channels among which
- * y holds an infinity or NaN become NaN.  Arguments and errors as in rda_mla_append.
+ * y holds an infinity or NaN become NaN.  Arguments and errors as in rda_mla_append;
+ * a position that two rows of one call go to is left with bytes of either.
  */
 rda_status rda_mla_append_q4(const void* kv, int64_t kv_stride, const float* weight, float eps,
                              const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,

@@ -34,6 +34,13 @@ def spread(n, low, high, seed):
     ([5000] + [1] * 30, 1, 8),             # one long, many short
     (spread(40, 1, 200, 6), 5, 32),        # three blocks of 64 rows a sequence
     ([1] * 3, 1, 40), ([31, 32, 33, 64, 65], 1, 65),
+    (spread(64, 1, 300, 9), 1, 8),         # as many sequences as a wave plans by itself
+    (spread(65, 1, 300, 9), 1, 8),
+    (spread(64, 1500, 2500, 10), 1, 2),    # longer shares: two workgroups a CU
+    (spread(2, 2000, 4000, 11), 1, 32),    # 64 query rows with many pieces each, joined by 16 waves
+    (spread(5, 900, 2000, 12), 1, 13),     # 65 of them: by 4
+    (spread(16, 900, 2000, 13), 1, 32),    # 512
+    (spread(19, 900, 2000, 14), 1, 27),    # 513: by one
 ])
 def test_shares(dev, lens, T, H):
     run(dev, lens, T, H, 32, seed=len(lens) + T)
@@ -46,6 +53,9 @@ def test_shares(dev, lens, T, H):
     ([40, 3], 1, 64, 700),                 # 64 rows a sequence, the prefix for 32 at a time
     (spread(130, 1, 50, 8), 1, 32, 2100),   # 32 rows a sequence, the prefix for 64 at a time
     ([0, 0], 2, 3, 33),
+    ([9] * 16, 1, 32, 5000),               # equal pieces of each block of query rows
+    ([9] * 33, 1, 40, 1100),               # blocks of 64 rows, which cross sequences
+    ([70, 0, 3], 1, 5, 2000),              # few rows: short pieces
 ])
 def test_prefixes(dev, lens, T, H, prefix):
     run(dev, lens, T, H, 16, seed=len(lens) + T, prefix=prefix)
@@ -66,7 +76,7 @@ def test_long(dev, lens, T, H, page, prefix):
     o, lse = compare(q, cache, table, kl, pre, prefix, lens)
 
 
-@pytest.mark.parametrize("page,apart", [(8, 16), (64, 400 * 64), (16, 1 << 20)])
+@pytest.mark.parametrize("page,apart", [(8, 16), (64, 400 * 64), (16, 1 << 20), (1 << 16, 0)])
 def test_pages_apart(dev, page, apart):
     """Pages that lie in a larger allocation, what is between them NaN."""
     say(f"[mla q4] pages of {page} rows, {apart} bytes between")
