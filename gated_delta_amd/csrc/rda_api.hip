@@ -199,7 +199,7 @@ rda_status mla_decode_any(bool q4, const void* q, const void* cache, int64_t pag
     if (prefix_len > 0 && num_pages == 0) return RDA_ERR_SHAPE;
     // row numbers are 32 bits in the kernel, those of the tiles that it fetches
     // (as zeros) behind the last too: up to nine tiles of 32 (q4: that it looks up,
-    // 72); q4 counts six tiles more for each sequence and block of query rows
+    // 72); q4 counts six tiles more for each sequence and 32 query rows
     if (int64_t(table_width) * page_tokens > (int64_t(1) << 31) - (q4 ? 4096 : 1024) ||
         !mla_tiles_ok((int64_t(tokens) * num_heads + 31) / 32 * 32 * batch,
                       int64_t(table_width) * page_tokens + (q4 ? 6 * 32 : 0)))

@@ -32,9 +32,9 @@
 // Bound by: the waits between those stages.  Of 3700 cycles for two tiles of a CU's
 // two workgroups 1090 are matrix instructions and 1650 LDS transfers (an unpacked
 // granule costs 13 cycles to write and 2 a row to read transposed).
-//   256 sequences of 512 to 8192 rows, 32 query rows: 138 us of which the joining takes
-//     10; 474 MB, 3.4 TB/s (78 us at 6.1)
-//   32 of them, 96 query rows: 65 us
+//   256 sequences of 512 to 8192 rows, 32 query rows: 136 us of which the joining takes
+//     10; 474 MB, 3.5 TB/s (78 us at 6.1)
+//   32 of them, 96 query rows: 64 us
 //   12288 query rows behind 16384 shared rows: 457 us, 975 TFLOP/s
 //   one sequence of 131072 rows: 38 us; of 1000: 16.5
 // Not faster: values read transposed as codes with the scale as an exponent added to
@@ -62,8 +62,12 @@ constexpr int kJoinThreads = 256;
 // start); 256 rows with 128 pieces 37 us for 43 with one wave, 512 rows with 64 pieces
 // equal, 2048 rows with 2 pieces 40 for 37.
 constexpr int kWideRows = kQ4FewRows, kFourRows = 512;
-// What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us).
-constexpr int kPieceTiles = 6;
+// What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us), in
+// tiles.  60 sequences of 500 to 4000 rows, 2 tokens: 49 us at 3, 46.8 at 6, 44.4 at 8;
+// 256 of one token 147, 143 and 146.  (The limits that the caller checks count 6 for each
+// 32 query rows.)
+template <int kRW>
+constexpr int kPieceTiles = kRW == 2 ? 8 : 6;
 // Shares of fewer tiles than this for two workgroups a CU are made twice as long for
 // one: half the pieces to write and join, but no second workgroup to fill a tile's
 // waits.  65536 rows (4 tiles) 32.6 us for 35.7, 16 x 2048 27.4 for 31.8; 131072 (8)
@@ -630,7 +634,7 @@ __device__ __forceinline__ void walk_sequences(const MlaDecodeArgs& A, Lds<kRW>&
     // again, as much as kPieceTiles tiles.  So the line that is cut into equal
     // shares holds that many places before each unit's tiles.
     const int n0 = tiles_at(lane);
-    int head = kPieceTiles, before0;
+    int head = kPieceTiles<kRW>, before0;
     auto places = [&](int n) { return n > 0 ? n + head : 0; };
     int x0 = places(n0);
     int total0 = block_sum(x0, before0);
