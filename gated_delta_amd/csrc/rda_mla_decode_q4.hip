@@ -56,12 +56,13 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;                        // cached rows per tile
 constexpr int kTileBytes = kTile * kQ4Row;       // 12800
 constexpr int kJoinThreads = 256;
-// How many waves join a query row: 16 (32 parts of 64 channels) up to the first number
-// of rows, 4 up to the second, else one.  64 rows with 256 pieces 41 us in all for 46
-// with four waves, but 128 rows 53 for 47.5 (workgroups of 1024 threads are slow to
-// start); 256 rows with 128 pieces 37 us for 43 with one wave, 512 rows with 64 pieces
-// equal, 2048 rows with 2 pieces 40 for 37.
-constexpr int kWideRows = kQ4FewRows, kFourRows = 512;
+// How many waves join a query row: 16 times 8 or 4 slices of channels up to the first
+// and second number of rows (256 workgroups each), 4 up to the third, else one.  64 rows
+// with 256 pieces 40 us in all for 45.5 with four waves (with 31 pieces 19.4 for 17.6),
+// but 128 rows 22.4 for 19.8; workgroups of 1024 threads are slow to start, a second one
+// on each CU (64 rows in 8 slices) costs 2 us.  256 rows with 128 pieces 37 us for 43
+// with one wave, 512 rows with 64 pieces equal, 2048 rows with 2 pieces 40 for 37.
+constexpr int kEightRows = 32, kWideRows = kQ4FewRows, kFourRows = 512;
 // What a unit costs a workgroup beside its tiles (queries in, sums out: 7 to 8 us), in
 // tiles.  60 sequences of 500 to 4000 rows, 2 tokens: 49 us at 3, 46.8 at 6, 44.4 at 8;
 // 256 of one token 147, 143 and 146.  (The limits that the caller checks count 6 for each
@@ -942,9 +943,14 @@ hipError_t launch_mla_decode_q4(const MlaDecodeArgs& A, hipStream_t stream) {
         if (hipError_t e = go(A.prefix_waves, true, false); e != hipSuccess) return e;
     if (hipError_t e = go(A.row_waves, together, true); e != hipSuccess) return e;
     const int rows = A.batch * A.tokens * A.heads;
-    if (rows <= kWideRows) mla_join_parts_q4_kernel<2, 32, 32><<<dim3(unsigned(rows * 8)), dim3(1024), 0, stream>>>(A);
-    else if (rows <= kFourRows) mla_join_parts_q4_kernel<8, 64, 4><<<dim3(unsigned(rows)), dim3(256), 0, stream>>>(A);
-    else mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
+    if (rows <= kEightRows)
+        mla_join_parts_q4_kernel<2, 32, 32><<<dim3(unsigned(rows * 8)), dim3(1024), 0, stream>>>(A);
+    else if (rows <= kWideRows)
+        mla_join_parts_q4_kernel<4, 32, 32><<<dim3(unsigned(rows * 4)), dim3(1024), 0, stream>>>(A);
+    else if (rows <= kFourRows)
+        mla_join_parts_q4_kernel<8, 64, 4><<<dim3(unsigned(rows)), dim3(256), 0, stream>>>(A);
+    else
+        mla_join_q4_kernel<<<dim3(unsigned((rows + 3) / 4)), dim3(kJoinThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 

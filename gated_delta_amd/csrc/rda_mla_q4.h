@@ -109,9 +109,9 @@ __device__ __forceinline__ void q4_acc_settle() {
 constexpr int kQ4Fetch = 4;
 #define RDA_Q4_ROWS(how)                                                             \
     "s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" how           \
-    "\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024" how                            \
-    "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048" how                            \
-    "\n\ts_mov_b64 exec, 0xff\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072" how   \
+    "\n\tglobal_load_lds_dwordx4 %1, %2 offset:0x400" how                            \
+    "\n\tglobal_load_lds_dwordx4 %1, %2 offset:0x800" how                            \
+    "\n\ts_mov_b64 exec, 0xff\n\tglobal_load_lds_dwordx4 %1, %2 offset:0xc00" how   \
     "\n\ts_mov_b64 exec, -1"
 
 template <bool kOnce>
