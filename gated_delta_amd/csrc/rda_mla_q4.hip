@@ -168,14 +168,15 @@ __device__ __forceinline__ Quantised quantise(const double* y) {
 // The norm in 32 bits, off by less than 2^-20 (eight products and six sums of
 // positive terms in the mean, half of that in its root, the root's own 2^-23,
 // five more roundings).  False where that may leave another code or scale:
-// where values 2^-17 smaller and larger do not agree, or out of the ordinary range.
+// where values 2^-17 smaller and larger do not agree, or out of the ordinary range:
+// also where a value is NaN though the sum is not, by a weight that is not finite.
 __device__ __forceinline__ bool quantise_normed(const float* x, const f32x4* wt, float eps, Quantised& q) {
     float ss = 0.f, y[8], most = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         ss = fmaf(x[i], x[i], ss);
         y[i] = x[i] * wt[i >> 2][i & 3];
-        most = fmaxf(most, fabsf(y[i]));
+        most = __builtin_elementwise_maximum(most, fabsf(y[i]));   // (NaN if one is)
     }
     ss = dpp_sum16(ss);
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(ss), __float_as_uint(ss), false, false);
