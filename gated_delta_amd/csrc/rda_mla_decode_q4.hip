@@ -241,8 +241,10 @@ __device__ __forceinline__ void take_query(Query& Q, uint32_t at, const uint32_t
     Q.scale = scales[row];
 }
 
-// The reference of a row that has seen no score.
-constexpr float kNone = -3e38f;
+// The reference of a row that has seen no score: any score outgrows it, however small
+// the scale is ((score + infinity) c is infinite for every c > 0, subnormal ones too),
+// and a row of masked places alone does not (NaN compares as no).
+constexpr float kNone = -INFINITY;
 
 // One piece: tiles [t0, t1) of a source for 32 kRW query rows.
 template <int kRW, bool kCausal>
