@@ -75,21 +75,20 @@ __device__ __forceinline__ void q4_acc_product(bf16x8 a, bf16x8 b) {
 }
 // The scores' products, in ordinary registers for the same reason: 16 cached rows
 // by 16 query rows, 128 channels (product kN of 4: group kN of each lane's four,
-// whose scale is byte kN of the row's, with scale byte kScale of the query's), and
-// 32 of the shared channels.  The query's operands stay in accumulation registers.
+// whose scales are byte kN of the row's and of the query's), and 32 of the shared
+// channels.  The query's operands stay in accumulation registers.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-template <int kN, int kScale>
+template <int kN>
 __device__ __forceinline__ void q4_score(f32x4& d, u32x4 a, i32x8 b, uint32_t as, uint32_t bs) {
     if constexpr (kN == 0)
         asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, 0, %3, %4 "
-                     "op_sel:[0,%5,0] op_sel_hi:[0,0,0] cbsz:4"
-                     : "=&v"(d) : "v"(a), "a"(b), "v"(as), "v"(bs), "n"(kScale) : RDA_Q4_ACC);
+                     "op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4"
+                     : "=&v"(d) : "v"(a), "a"(b), "v"(as), "v"(bs) : RDA_Q4_ACC);
     else
         asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 "
-                     "op_sel:[%6,%5,0] op_sel_hi:[%7,0,0] cbsz:4"
-                     : "+v"(d) : "v"(a), "a"(b), "v"(as), "v"(bs), "n"(kScale), "n"(kN & 1), "n"(kN >> 1)
-                     : RDA_Q4_ACC);
+                     "op_sel:[%5,%5,0] op_sel_hi:[%6,%6,0] cbsz:4"
+                     : "+v"(d) : "v"(a), "a"(b), "v"(as), "v"(bs), "n"(kN & 1), "n"(kN >> 1) : RDA_Q4_ACC);
 }
 __device__ __forceinline__ void q4_score_pe(f32x4& d, bf16x8 a, bf16x8 b) {
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b) : RDA_Q4_ACC);

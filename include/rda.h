@@ -667,10 +667,12 @@ size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t 
  * rda_mla_decode over the 4-bit cache (page_stride in bytes; every other
  * argument, limit and error as there, but table_width x page_tokens at most
  * 2^31 - 4096, with 192 more in the limit on the product).  The query is used
- * as it is: in the products with the codes it is a pair of 8-bit values with
- * scales of the row's largest magnitude, together off by at most 2^-22 of that
- * (or 2^-118, if that is more).  A query row whose latent part holds an
- * infinity or NaN, and one that sees a row with a NaN group, gives NaN
+ * as it is: in the products with the codes it is a pair of 8-bit values with a
+ * scale for each 32 channels, whose largest magnitude is M (counted as 2^-109 at
+ * least).  Channels of M / 64 or more enter exactly; the product of a smaller one
+ * with a cached value v, whose group has the unit u = 2^(s - 127), is off by at
+ * most 2^-14 M (|v| / 2 + u).  Sums have 24 bits.  A query row whose latent part
+ * holds an infinity or NaN, and one that sees a row with a NaN group, gives NaN
  * throughout; rows that it does not see do not reach it.
  */
 rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
