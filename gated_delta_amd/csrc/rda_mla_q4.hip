@@ -5,7 +5,8 @@
 //   y_c = x_c / sqrt(mean_{c' < 512} x_c'^2 + eps) * weight_c  (or x_c),
 //   e   = the least integer with max |y| <= 7 2^e over y_c's group of 32,
 //   code = y / 2^e rounded to nearest on 0, 1/2, 1, 3/2, 2, 3, 4, 6 (ties to the
-//   even code; 7 goes to 6: no value moves further than half a step).
+//   even code; 7 goes to 6: no value moves further than half a step, but for those
+//   above 7 2^125, the largest exponent's, which go to 6 2^125).
 // y, e and the codes are as 64 bits give them: a step is a quarter or more of a
 // value, so a code must not depend on how a sum was ordered.  With a norm 32 bits
 // are tried first (quantise_normed), and decide all codes of 99 rows in 100.

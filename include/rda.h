@@ -628,8 +628,9 @@ rda_status rda_mla_append(const void* kv, int64_t kv_stride, const float* weight
  *     code = y_c / 2^e rounded to nearest (ties to the even code, the largest
  *            is 6)
  *
- * where y, e and the rounding are computed in 64 bits.  No value moves further
- * than half a step between neighbouring codes of its group.  32 channels among which
+ * where y, e and the rounding are computed in 64 bits.  No value up to 7 x 2^125
+ * moves further than half a step between neighbouring codes of its group; larger
+ * ones become 6 x 2^125.  32 channels among which
  * y holds an infinity or NaN become NaN.  Arguments and errors as in rda_mla_append;
  * a position that two rows of one call go to is left with bytes of either.
  */

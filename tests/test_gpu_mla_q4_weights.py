@@ -39,3 +39,16 @@ def test_bad_weight_on_zero(dev, bad):
     kv[::3, 256:288] = 0.0
     weight[[64, 130, 270]] = bad
     append(dev, kv, [24], [24], 8, weight)
+
+
+@pytest.mark.parametrize("weight,eps", [(2.0 ** 124, 1e-5), (2.0 ** 126, 0.0), (3.4e38, 1e-5)])
+def test_largest_values(dev, weight, eps):
+    """Values beyond 7 x 2^125 become 6 x 2^125; no finite value becomes NaN."""
+    say(f"[append q4] weights of {weight}")
+    kv = rows(20, 24)
+    kv[::4, 70] = 30.0                     # beside small ones
+    kv[5:9] *= 1e-30
+    w = torch.full((512,), weight) * torch.where(torch.arange(512) % 3 == 0, -1.0, 1.0)
+    got, table, _, _ = append(dev, kv, [20], [20], 8, w, eps=eps)
+    assert int(got[table[0].long().to(dev)].reshape(-1, 400)[:20, 256:272].max()) == 125 + 127
+    append(dev, torch.full((3, 576), 3.3895e38).bfloat16(), [3], [3], 8, None)
