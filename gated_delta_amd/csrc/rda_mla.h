@@ -121,4 +121,19 @@ __device__ __forceinline__ void raw_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// The sequence of packed row t: the last n with cu[n] <= t.  64 boundaries a step,
+// so a batch of 64 costs one load latency and one of 4096 two.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, int l) {
+    int lo = 0, n = num_seqs;   // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int at = lo + l * step;
+        const uint64_t below = __ballot(at < lo + n && cu[at < num_seqs ? at : 0] <= t);
+        const int k = below ? 63 - __builtin_clzll(below) : 0;
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
 }  // namespace rda

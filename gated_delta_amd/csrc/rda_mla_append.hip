@@ -18,21 +18,6 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// The sequence of token t: the last n with cu[n] <= t.  64 boundaries a step,
-// so a batch of 64 costs one load latency and one of 4096 two.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, int l) {
-    int lo = 0, n = num_seqs;   // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 63) / 64;
-        const int at = lo + l * step;
-        const uint64_t below = __ballot(at < lo + n && cu[at < num_seqs ? at : 0] <= t);
-        const int k = below ? 63 - __builtin_clzll(below) : 0;
-        n = min(step, n - k * step);
-        lo += k * step;
-    }
-    return lo;
-}
-
 __global__ __launch_bounds__(64 * kWaves) void mla_append_kernel(const MlaAppendArgs A) {
     const int l = threadIdx.x & 63;
     const int t = blockIdx.x * kWaves + wave_id();

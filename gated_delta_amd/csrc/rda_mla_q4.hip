@@ -23,20 +23,6 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// The sequence of row t: the last n with cu[n] <= t, 64 boundaries a step.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int t, int l) {
-    int lo = 0, n = num_seqs;   // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 63) / 64;
-        const int at = lo + l * step;
-        const uint64_t below = __ballot(at < lo + n && cu[at < num_seqs ? at : 0] <= t);
-        const int k = below ? 63 - __builtin_clzll(below) : 0;
-        n = min(step, n - k * step);
-        lo += k * step;
-    }
-    return lo;
-}
-
 // Where the kRows rows from `t` on lie in the cache, looked up by a lane each.
 struct Places {
     uint64_t at;     // lane r: row t + r's address, 0 where it has none
