@@ -672,9 +672,11 @@ size_t rda_mla_decode_q4_workspace_bytes(int32_t batch, int32_t tokens, int32_t 
  * scale for each 32 channels, whose largest magnitude is M (counted as 2^-109 at
  * least).  Channels of M / 64 or more enter exactly; the product of a smaller one
  * with a cached value v, whose group has the unit u = 2^(s - 127), is off by at
- * most 2^-14 M (|v| / 2 + u).  Sums have 24 bits.  A query row whose latent part
- * holds an infinity or NaN, and one that sees a row with a NaN group, gives NaN
- * throughout; rows that it does not see do not reach it.
+ * most 2^-14 M (|v| / 2 + u).  Sums have 24 bits; where scores pass 2^28 or the
+ * sum of |v| over a query's rows 2^119, results may be infinite or NaN (as over
+ * bf16).  A query row whose latent part holds an infinity or NaN, and one that
+ * sees a row with a NaN group, gives NaN throughout; rows that it does not see do
+ * not reach it.
  */
 rda_status rda_mla_decode_q4(const void* q, const void* cache, int64_t page_stride, int32_t num_pages,
                              int32_t page_tokens, const int32_t* block_table, int32_t table_width,
