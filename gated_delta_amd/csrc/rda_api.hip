@@ -131,7 +131,7 @@ size_t mla_decode_plan(MlaDecodeArgs& A, unsigned char* ws, bool q4 = false) {
     const int most_waves = q4 ? 2 : 4, workgroups = q4 ? kQ4Workgroups : kMlaWorkgroups;
     A.row_waves = unit_rows > 64 ? most_waves : unit_rows > 32 ? 2 : 1;
     A.row_blocks = int32_t((unit_rows + 32 * A.row_waves - 1) / (32 * A.row_waves));
-    A.min_tiles = q4 ? 2 : 4;   // (and no more than an average unit has: see the kernel)
+    A.min_tiles = q4 ? 2 : 4;   // (over bf16 no more than an average unit has: see its kernel)
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* p = ws ? ws + at : nullptr;
