@@ -35,11 +35,11 @@
 // Bound by: the waits between those stages.  Of 3700 cycles for two tiles of a CU's
 // two workgroups 1090 are matrix instructions and 1650 LDS transfers (an unpacked
 // granule costs 13 cycles to write and 2 a row to read transposed).
-//   256 sequences of 512 to 8192 rows, 32 query rows: 136 us of which the joining takes
-//     10; 474 MB, 3.5 TB/s (78 us at 6.1)
+//   256 sequences of 512 to 8192 rows, 32 query rows: 132 us of which the joining takes
+//     10; 474 MB, 3.6 TB/s (78 us at 6.1)
 //   32 of them, 96 query rows: 64 us
-//   12288 query rows behind 16384 shared rows: 457 us, 975 TFLOP/s
-//   one sequence of 131072 rows: 38 us; of 1000: 16.5
+//   12288 query rows behind 16384 shared rows: 453 us, 985 TFLOP/s
+//   one sequence of 131072 rows: 38 us; of 777: 16
 // Not faster: values read transposed as codes with the scale as an exponent added to
 // the probability (158.6 us for the first case and 577 for the third, both 10 %
 // slower: 220 ordinary instructions a wave and tile for 160); 128 query rows a
